@@ -248,6 +248,89 @@ wq_status wq_gemm_gate_up(const void* x, wq_dtype dt, const void* packed, wq_qmo
  */
 wq_status wq_hadamard(const void* x, wq_dtype dt, void* y, int M, int K, int block, void* stream);
 
+/*
+ * ---- 4-bit key/value cache -------------------------------------------------
+ * At 2-4 bit weights the key/value cache is the larger part of what a decoded
+ * token of a long context reads.  These entry points hold it in 4 bits beside
+ * the weights: rows are quantised as they are written, and attention multiplies
+ * the codes themselves.
+ *
+ * Cache of one layer: `num_pages` pages of `page_size` tokens for `kv_heads`
+ * heads of `head_dim` channels, wq_kv_cache_bytes() bytes, 128-byte aligned, in
+ * the kernels' own layout (nothing needs to start at any value).  A group of
+ * `group` channels x of one token and head is held as
+ *     lo = min x,  s = RN((max x - min x) / 15)    in the model's 16-bit type,
+ *     c = floor((x - lo) / s + 1/2) in 0..15        (0 where s == 0),
+ * with x - lo rounded to fp32, and stands for lo + s c.  A group that holds an
+ * infinity or a NaN stands for NaN.
+ *   head_dim  64, 96, 128, 192 or 256; group 32, 64 or 128, dividing head_dim;
+ *   page_size a power of two from 16 to 1024; kv_heads <= 1024
+ *   (other values: WQ_EUNSUPPORTED; group not dividing head_dim: WQ_EINVAL).
+ *
+ * Sequences: every call takes `rows` rows of `batch` sequences.  cu_q (device,
+ * int32 [batch + 1], ascending) gives the row each sequence starts at; NULL
+ * means rows / batch rows each (rows % batch == 0).  kv_lens (device, int32
+ * [batch]) is each sequence's length with these rows included: they are its
+ * last ones, row i of n at position kv_len - n + i.  block_table (device, int32
+ * [batch][max_pages]) names the page of positions page_size p .. + page_size-1.
+ * Nothing read from device memory leads outside the buffers: lengths are held
+ * to 0 .. max_pages * page_size and row offsets to 0 .. rows; positions whose
+ * page number is not in 0 .. num_pages - 1, or that lie below 0, are no place:
+ * nothing is written there, they read as zero and attention does not see them.
+ * Rows outside every sequence (before cu_q[0], from cu_q[batch] on) are left as
+ * they were.
+ * Row matrices are [rows][heads][head_dim] with heads contiguous and `ld_*`
+ * elements between rows (a multiple of 8; 16-byte aligned base), so q, k and v
+ * can be slices of one fused projection's output.
+ */
+
+/* Size in bytes of a cache; 0 for unsupported arguments. */
+size_t wq_kv_cache_bytes(int num_pages, int page_size, int kv_heads, int head_dim, int group);
+
+/*
+ * wq_kv_write -- quantise the rows of k and v into their places.  Everything
+ * else in the cache keeps its value.  A page that receives rows must belong to
+ * one sequence only (places written twice in a call, or by calls that overlap
+ * in time within 16 aligned positions, hold unspecified values).
+ */
+wq_status wq_kv_write(const void* k, const void* v, int64_t ld_k, int64_t ld_v, wq_dtype dt, void* cache,
+                      const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_q, int rows, int batch,
+                      int max_pages, int num_pages, int page_size, int kv_heads, int head_dim, int group,
+                      void* stream);
+
+/*
+ * wq_kv_read -- the cached values lo + s c of the rows' places, rounded to
+ * `dt` (the type they were written in) once.
+ */
+wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t ld_v, wq_dtype dt,
+                     const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_q, int rows, int batch,
+                     int max_pages, int num_pages, int page_size, int kv_heads, int head_dim, int group,
+                     void* stream);
+
+/*
+ * wq_kv_attention -- out = softmax(scale q K^T) V over the cached values, for
+ * prefill, chunks and single tokens alike.
+ *   q, out : [rows][q_heads][head_dim] in `dt`, the type of the cache; head h
+ *            attends with kv head h / (q_heads / kv_heads)
+ *   scale  : positive and finite
+ *   causal : 1: a row sees the positions up to its own; 0: its whole sequence
+ *   window : > 0: only the last `window` positions up to its own (0: all)
+ *   max_kv_len : the longest kv_len to expect; it shapes the launch only (the
+ *            result is right for any lengths)
+ *   ws     : wq_kv_workspace_bytes() bytes, 16-byte aligned (may be NULL when 0)
+ * A row that sees no position is zero.  Scores, softmax and sums are fp32; the
+ * product of a probability and a value step is rounded to fp16 once, and the
+ * output to `dt` once.  Value steps s are expected in 2^-60 .. 2^100 (smaller
+ * ones lose bits).  The same call gives the same bits.
+ */
+size_t wq_kv_workspace_bytes(int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim,
+                             int max_kv_len);
+wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* cache, const int32_t* block_table,
+                          const int32_t* kv_lens, const int32_t* cu_q, void* out, int64_t ld_out, int rows, int batch,
+                          int max_pages, int num_pages, int page_size, int q_heads, int kv_heads, int head_dim,
+                          int group, float scale, int causal, int window, int max_kv_len, void* ws, size_t ws_bytes,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,6 +63,17 @@ def lib() -> ctypes.CDLL:
         L.wq_gemm_noalloc.restype = I
         L.wq_hadamard.argtypes = [P, I, P, I, I, I, P]
         L.wq_hadamard.restype = I
+        L64, F = ctypes.c_int64, ctypes.c_float
+        L.wq_kv_cache_bytes.argtypes = [I] * 5
+        L.wq_kv_cache_bytes.restype = Z
+        L.wq_kv_write.argtypes = [P, P, L64, L64, I, P, P, P, P] + [I] * 8 + [P]
+        L.wq_kv_write.restype = I
+        L.wq_kv_read.argtypes = [P, P, P, L64, L64, I, P, P, P] + [I] * 8 + [P]
+        L.wq_kv_read.restype = I
+        L.wq_kv_workspace_bytes.argtypes = [I] * 7
+        L.wq_kv_workspace_bytes.restype = Z
+        L.wq_kv_attention.argtypes = [P, L64, I, P, P, P, P, P, L64] + [I] * 9 + [F, I, I, I, P, Z, P]
+        L.wq_kv_attention.restype = I
         if L.wq_layout_version() != LAYOUT_VERSION:
             raise RuntimeError("libwq.so layout version does not match this binding")
         _lib = L
@@ -369,3 +380,7 @@ def linear(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None) 
     if layer.gate_up:
         return (wq_gemv_gate_up if small else wq_gemm_gate_up)(x, layer, out, ws, stream)
     return (wq_gemv if small else wq_gemm)(x, layer, out, ws, stream)
+
+
+from .kvcache import (KVCache, wq_kv_attention, wq_kv_cache, wq_kv_cache_bytes, wq_kv_read,  # noqa: E402
+                      wq_kv_workspace_bytes, wq_kv_write)

@@ -12,7 +12,11 @@ LIB = os.path.join(HERE, "libwq.so")
 PROBE_LIB = os.path.join(HERE, "libwq_probe.so")
 # (source, object name, extra defines): the kernel files are compiled once
 # per (activation dtype, code width) so the instantiations build in parallel.
-SOURCES = [("wq_api.hip", "wq_api", []), ("wq_hadamard.hip", "wq_hadamard", [])]
+SOURCES = [("wq_api.hip", "wq_api", []), ("wq_hadamard.hip", "wq_hadamard", []), ("wq_kv_api.hip", "wq_kv_api", []),
+           ("wq_kv_rows.hip", "wq_kv_rows", [])]
+# the cache attention once per head size
+for _d in (256, 192, 128, 96, 64):
+    SOURCES.append(("wq_kv_attention.hip", f"wq_kv_attention_{_d}", [f"-DWQ_HEAD_DIM={_d}"]))
 for _k in ("wq_gemv", "wq_gemm"):
     for _dt, _dn in ((0, "f16"), (1, "bf16")):
         for _b in (2, 3, 4):
