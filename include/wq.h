@@ -199,6 +199,29 @@ wq_status wq_gemm_noalloc(const void* x, wq_dtype dt, const void* packed, wq_qmo
                           int bits, int group_size, void* stream);
 
 /*
+ * wq_gemv_epilogue / wq_gemm_epilogue -- the same products with the rest of a
+ * linear layer in their epilogue:
+ *     y = act(x . dequant(W) + bias) + residual
+ * in fp32, rounded to `dt` once.
+ *   bias     : device [N] in `dt`, or NULL
+ *   act      : none, ReLU, SiLU v / (1 + e^-v), or GELU in its tanh form
+ *              0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))
+ *   residual : device [M][N] in `dt`, or NULL; it may be y itself (the sum is
+ *              then formed in place), other overlaps with y are WQ_EINVAL
+ * bias and residual are 16-byte aligned.  Other arguments, limits and workspace
+ * as for wq_gemv / wq_gemm; the buffer is one from wq_repack (a gate+up layer's
+ * columns are interleaved).  Without bias, activation and residual these are
+ * wq_gemv and wq_gemm.
+ */
+typedef enum { WQ_ACT_NONE = 0, WQ_ACT_RELU = 1, WQ_ACT_SILU = 2, WQ_ACT_GELU = 3 } wq_act;
+wq_status wq_gemv_epilogue(const void* x, wq_dtype dt, const void* packed, wq_qmode mode, const uint16_t* lut,
+                           const int32_t* perm, const void* bias, wq_act act, const void* residual, void* y, int M,
+                           int N, int K, int bits, int group_size, void* ws, size_t ws_bytes, void* stream);
+wq_status wq_gemm_epilogue(const void* x, wq_dtype dt, const void* packed, wq_qmode mode, const uint16_t* lut,
+                           const int32_t* perm, const void* bias, wq_act act, const void* residual, void* y, int M,
+                           int N, int K, int bits, int group_size, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Activation-fused gate+up layer.  The Triton GPTQ page fuses the feed-forward
  * layers ("How It Works") without naming the activation; these entry points
  * read it as the gated SiLU of LLaMA-style blocks: for a weight W = [gate | up]

@@ -193,3 +193,46 @@ def test_reference_attention_is_softmax():
         a = torch.softmax(q[i].double() @ K[:5 + i].T * 0.2, 1) @ V[:5 + i]
         assert torch.allclose(a, out[i], atol=1e-12)
     assert float(bound.max()) < 0.02
+
+
+# ---------------------------------------------------------------------------
+# Epilogue products
+# ---------------------------------------------------------------------------
+def epilogue_call(L, fn, bias=16, act=0, res=16, y=1 << 20, M=1, N=4096, K=4096, x=16):
+    return getattr(L, fn)(P(x), 0, P(16), 0, None, None, P(bias), act, P(res), P(y), M, N, K, 4, 128, None, 0, None)
+
+
+@pytest.mark.parametrize("fn", ["wq_gemv_epilogue", "wq_gemm_epilogue"])
+def test_epilogue_refusals(L, fn):
+    assert epilogue_call(L, fn, M=0) == 0
+    assert epilogue_call(L, fn, act=4) == 1
+    assert epilogue_call(L, fn, act=-1) == 1
+    assert epilogue_call(L, fn, bias=24) == 2                      # misaligned
+    assert epilogue_call(L, fn, res=24) == 2
+    assert epilogue_call(L, fn, res=(1 << 20) + 16) == 1           # overlaps y without being y
+    assert epilogue_call(L, fn, res=(1 << 20) - 16) == 1
+    assert epilogue_call(L, fn, x=None) == 1
+    assert epilogue_call(L, fn, N=4104) == 2
+    assert epilogue_call(L, "wq_gemv_epilogue", M=33) == 2
+
+
+def test_epilogue_binding_refuses(L):
+    nbytes = wq.wq_packed_bytes(256, 64, 4, 128, wq.SYM)
+    layer = wq.PackedLayer(torch.zeros(nbytes, dtype=torch.uint8), 256, 64, 4, 128, wq.SYM)
+    x = torch.zeros(2, 256, dtype=torch.float16)
+    half = dict(dtype=torch.float16)
+    with pytest.raises(ValueError, match="act must be"):
+        wq.linear(x, layer, act="tanh")
+    with pytest.raises(ValueError, match="bias must have shape"):
+        wq.linear(x, layer, bias=torch.zeros(63, **half))
+    with pytest.raises(ValueError, match="bias must have dtype"):
+        wq.linear(x, layer, bias=torch.zeros(64))
+    with pytest.raises(ValueError, match="residual must have shape"):
+        wq.linear(x, layer, residual=torch.zeros(1, 64, **half))
+    with pytest.raises(ValueError, match="residual must be contiguous"):
+        wq.wq_gemm_epilogue(x, layer, residual=torch.zeros(64, 2, **half).t())
+    fused = wq.PackedLayer(layer.packed, 256, 64, 4, 128, wq.SYM, gate_up=True)
+    with pytest.raises(ValueError, match="wq_repack"):
+        wq.linear(x, fused, bias=torch.zeros(64, **half))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        wq.linear(x, layer, bias=torch.zeros(64, **half))

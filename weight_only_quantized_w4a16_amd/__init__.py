@@ -59,6 +59,10 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.argtypes = [P, I, P, I, P, P, P, I, I, I, I, I, P, Z, P]
             f.restype = I
+        for name in ("wq_gemv_epilogue", "wq_gemm_epilogue"):
+            f = getattr(L, name)
+            f.argtypes = [P, I, P, I, P, P, P, I, P, P, I, I, I, I, I, P, Z, P]
+            f.restype = I
         L.wq_gemm_noalloc.argtypes = [P, I, P, I, P, P, P, I, I, I, I, I, P]
         L.wq_gemm_noalloc.restype = I
         L.wq_hadamard.argtypes = [P, I, P, I, I, I, P]
@@ -260,8 +264,12 @@ def wq_dequant_debug(layer: PackedLayer, dtype: torch.dtype, stream=None) -> tor
     return w
 
 
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+_ACTS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU}
+
+
 def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.Tensor],
-             ws: Optional[torch.Tensor], stream) -> torch.Tensor:
+             ws: Optional[torch.Tensor], stream, epilogue=None) -> torch.Tensor:
     # The kernels take raw pointers: a short or misplaced buffer would be read
     # or written out of bounds on the device, so everything is checked here,
     # before the library is called.
@@ -276,6 +284,15 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
     ncols = layer.N // 2 if fused else layer.N
     if out is not None:
         _check_tensor(out, "out", (x.dtype,), (M, ncols), x.device)
+    extra = ()
+    if epilogue is not None:
+        bias, act, residual = epilogue
+        _need(act in _ACTS, lambda: f"act must be None, 'none', 'relu', 'silu' or 'gelu', got {act!r}")
+        if bias is not None:
+            _check_tensor(bias, "bias", (x.dtype,), (ncols,), x.device)
+        if residual is not None:
+            _check_tensor(residual, "residual", (x.dtype,), (M, ncols), x.device)
+        extra = (_ptr(bias), _ACTS[act], _ptr(residual))
     need = wq_workspace_bytes(M, layer.N, layer.K, layer.bits, layer.perm is not None)
     if ws is not None and need:
         _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == x.device,
@@ -288,8 +305,9 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
     if need and ws is None:
         ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     rc = getattr(lib(), fn)(_ptr(x), _dt(x.dtype), _ptr(layer.packed), layer.mode, _ptr(layer.lut),
-                            _ptr(layer.perm), _ptr(out), M, layer.N, layer.K, layer.bits, layer.group_size,
-                            _ptr(ws) if need else None, need if need else 0, _stream(stream, x.device))
+                            _ptr(layer.perm), *extra, _ptr(out), M, layer.N, layer.K, layer.bits,
+                            layer.group_size, _ptr(ws) if need else None, need if need else 0,
+                            _stream(stream, x.device))
     _check(fn, rc)
     return out
 
@@ -302,6 +320,19 @@ def wq_gemv(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None)
 def wq_gemm(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None) -> torch.Tensor:
     """y = x . dequant(W) for any M (prefill)."""
     return _product("wq_gemm", x, layer, out, ws, stream)
+
+
+def wq_gemv_epilogue(x: torch.Tensor, layer: PackedLayer, bias=None, act=None, residual=None, out=None, ws=None,
+                     stream=None) -> torch.Tensor:
+    """y = act(x . dequant(W) + bias) + residual for 1 <= M <= 32; act None, "relu", "silu" or "gelu" (tanh form),
+    residual [M][N] (out may be the residual: in place)."""
+    return _product("wq_gemv_epilogue", x, layer, out, ws, stream, (bias, act, residual))
+
+
+def wq_gemm_epilogue(x: torch.Tensor, layer: PackedLayer, bias=None, act=None, residual=None, out=None, ws=None,
+                     stream=None) -> torch.Tensor:
+    """y = act(x . dequant(W) + bias) + residual for any M (see wq_gemv_epilogue)."""
+    return _product("wq_gemm_epilogue", x, layer, out, ws, stream, (bias, act, residual))
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # WQ_NOALLOC_SCRATCH_BYTES
@@ -373,10 +404,14 @@ def use_gemv(M: int, layer: PackedLayer) -> bool:
     return M <= GEMV_MAX_M
 
 
-def linear(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None) -> torch.Tensor:
+def linear(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None, *, bias=None, act=None,
+           residual=None) -> torch.Tensor:
     """Decode-sized M (use_gemv) goes to wq_gemv, larger M to wq_gemm (the
-    *_gate_up pair for a layer from wq_repack_gate_up)."""
+    *_gate_up pair for a layer from wq_repack_gate_up).  With bias, act or
+    residual: y = act(x . dequant(W) + bias) + residual (the *_epilogue pair)."""
     small = use_gemv(x.shape[0], layer)
+    if bias is not None or act not in (None, "none") or residual is not None:
+        return (wq_gemv_epilogue if small else wq_gemm_epilogue)(x, layer, bias, act, residual, out, ws, stream)
     if layer.gate_up:
         return (wq_gemv_gate_up if small else wq_gemm_gate_up)(x, layer, out, ws, stream)
     return (wq_gemv if small else wq_gemm)(x, layer, out, ws, stream)

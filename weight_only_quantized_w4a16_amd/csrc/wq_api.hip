@@ -401,11 +401,12 @@ wq_status wq_dequant_debug(const void* packed, wq_qmode mode, const uint16_t* lu
 
 static wq_status product(bool gemm, bool swiglu, const void* x, wq_dtype dt, const void* packed, wq_qmode mode,
                          const uint16_t* lut, const int32_t* perm, void* y, int M, int N, int K, int bits,
-                         int group_size, void* ws, size_t ws_bytes, void* stream) {
+                         int group_size, void* ws, size_t ws_bytes, void* stream, const Epilogue& epi = Epilogue()) {
   wq_status st = check_layer(K, N, bits, group_size, mode);
   if (st != WQ_OK) return st;
   if (M < 0) return WQ_EINVAL;
   if (dt != WQ_F16 && dt != WQ_BF16) return WQ_EINVAL;
+  if (epi.act < WQ_ACT_NONE || epi.act > WQ_ACT_GELU) return WQ_EINVAL;
   if (!gemm && M > 32) return WQ_EUNSUPPORTED;
   if (swiglu && N % 32 != 0) return WQ_EUNSUPPORTED;
   if (M == 0) return WQ_OK;
@@ -413,6 +414,10 @@ static wq_status product(bool gemm, bool swiglu, const void* x, wq_dtype dt, con
   if (mode == LUT && !lut) return WQ_EINVAL;
   if (perm && fine_zero_group(mode)) return WQ_EUNSUPPORTED;
   if (((uintptr_t)x | (uintptr_t)y | (uintptr_t)packed) & 15) return WQ_EUNSUPPORTED;
+  if (((uintptr_t)epi.bias | (uintptr_t)epi.residual) & 15) return WQ_EUNSUPPORTED;
+  // the residual is y itself (every element is read where it is written) or apart from it
+  const uintptr_t rb = (uintptr_t)epi.residual, yb = (uintptr_t)y, yn = (uintptr_t)M * N * 2;
+  if (rb && rb != yb && rb < yb + yn && yb < rb + yn) return WQ_EINVAL;
   if (M > (1 << 24)) return WQ_EUNSUPPORTED;
   if ((size_t)M * K * 2 >= ((size_t)1 << 31)) return WQ_EUNSUPPORTED;  // activation buffer offsets
   const int ksplit = gemm ? gemm_ksplit(M, N, K, bits) : 1;
@@ -435,6 +440,7 @@ static wq_status product(bool gemm, bool swiglu, const void* x, wq_dtype dt, con
   ProductArgs a{xin, (int)dt, packed, (int)mode, lut, y, M, N, K, bits, group_size, swiglu ? 1 : 0, s};
   a.ksplit = ksplit;
   a.part = ksplit > 1 ? (void*)((uint8_t*)ws + perm_ws_bytes(M, K, perm != nullptr)) : nullptr;
+  a.epi = epi;
   return launch_product(gemm, a);
 }
 
@@ -504,6 +510,20 @@ wq_status wq_gemm_gate_up(const void* x, wq_dtype dt, const void* packed, wq_qmo
                           const int32_t* perm, void* y, int M, int N, int K, int bits, int group_size, void* ws,
                           size_t ws_bytes, void* stream) {
   return product(true, true, x, dt, packed, mode, lut, perm, y, M, N, K, bits, group_size, ws, ws_bytes, stream);
+}
+
+wq_status wq_gemv_epilogue(const void* x, wq_dtype dt, const void* packed, wq_qmode mode, const uint16_t* lut,
+                           const int32_t* perm, const void* bias, wq_act act, const void* residual, void* y, int M,
+                           int N, int K, int bits, int group_size, void* ws, size_t ws_bytes, void* stream) {
+  return product(false, false, x, dt, packed, mode, lut, perm, y, M, N, K, bits, group_size, ws, ws_bytes, stream,
+                 Epilogue{(const uint16_t*)bias, (const uint16_t*)residual, (int)act});
+}
+
+wq_status wq_gemm_epilogue(const void* x, wq_dtype dt, const void* packed, wq_qmode mode, const uint16_t* lut,
+                           const int32_t* perm, const void* bias, wq_act act, const void* residual, void* y, int M,
+                           int N, int K, int bits, int group_size, void* ws, size_t ws_bytes, void* stream) {
+  return product(true, false, x, dt, packed, mode, lut, perm, y, M, N, K, bits, group_size, ws, ws_bytes, stream,
+                 Epilogue{(const uint16_t*)bias, (const uint16_t*)residual, (int)act});
 }
 
 wq_status wq_hadamard(const void* x, wq_dtype dt, void* y, int M, int K, int block, void* stream) {

@@ -60,6 +60,15 @@ inline wq_status launch_status() {
   return hipGetLastError() == hipSuccess ? WQ_OK : WQ_EHIP;
 }
 
+// What the epilogue products add to y = x . dequant(W) before its one rounding:
+// y = act(x W + bias) + residual.
+struct Epilogue {
+  const uint16_t* bias = nullptr;      // [N] or null
+  const uint16_t* residual = nullptr;  // [M][N] or null; may be y itself
+  int act = 0;                         // wq_act
+  bool on() const { return bias || residual || act; }
+};
+
 // Entry points of the product kernels (validated arguments only).
 struct ProductArgs {
   const void* x;            // activations [M][K] (already permuted for act-order)
@@ -77,6 +86,7 @@ struct ProductArgs {
   // workgroup and prefetch depth (0: the library's own choice, which every
   // entry point uses)
   int waves = 0, pf = 0;
+  Epilogue epi;             // plain layers only
 };
 #define WQ_CAT2(a, b) a##b
 #define WQ_CAT(a, b) WQ_CAT2(a, b)

@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/wq.h"
 #include "wq_layout.hpp"
 
 namespace wq {
@@ -73,6 +74,40 @@ __device__ inline uint32_t pack2(float lo, float hi) {
   } else {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, bf2));
   }
+}
+
+// Epilogue of a product: act(v + bias) + residual in fp32.  SiLU and GELU (its
+// tanh form, 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))) are both
+// v / (1 + e^-(a v + b v^3)), so one formula with two coefficients serves both;
+// for v far below zero the exponential is infinite and the quotient -0.
+struct EpilogueArgs {
+  const uint16_t *bias, *residual;
+  int act;
+  int on;
+};
+__device__ inline float activate(float v, int act) {
+  if (act == WQ_ACT_RELU) return v < 0.0f ? 0.0f : v;
+  if (act != WQ_ACT_NONE) {
+    const float a = act == WQ_ACT_SILU ? 1.0f : 1.5957691216057308f;
+    const float b = act == WQ_ACT_SILU ? 0.0f : 0.07135481282052307f;
+    return v / (1.0f + expf(-v * __builtin_fmaf(b, v * v, a)));
+  }
+  return v;
+}
+template <int DT>
+__device__ inline float elem_to_f32(uint16_t h) {
+  return DT == F16 ? f16_to_f32(h) : bf16_to_f32(h);
+}
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+// four consecutive outputs of row m, columns n .. n + 3 (n a multiple of 4)
+template <int DT>
+__device__ inline f4 epilogue4(f4 v, const EpilogueArgs& e, size_t at, int n) {
+  u16x4 b = {0, 0, 0, 0}, r = {0, 0, 0, 0};
+  if (e.bias) b = *(const u16x4*)(e.bias + n);
+  if (e.residual) r = *(const u16x4*)(e.residual + at);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = activate(v[i] + elem_to_f32<DT>(b[i]), e.act) + elem_to_f32<DT>(r[i]);
+  return v;
 }
 
 template <int DT>

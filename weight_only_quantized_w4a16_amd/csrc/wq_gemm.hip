@@ -48,6 +48,7 @@ struct GemmArgs {
   int swiglu;             // fused gate+up layer: y [M][N/2] = SiLU(gate) * up
   int ksplit, ktps;       // K split over ksplit workgroups of ktps k-tiles (1: no split)
   float* part;            // ksplit > 1: fp32 partial products [ksplit][M][N]
+  EpilogueArgs epi;       // plain layers: act(y + bias) + residual before the rounding
 };
 
 // s_waitcnt immediate (gfx9 encoding) that waits until at most n vector
@@ -333,7 +334,6 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = 1.0f;
     if constexpr (EPI_SCALE) {  // one scale record per column tile
-      typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
       const u16x4 sv = *(const u16x4*)(a.S + (size_t)(nt0 + t) * 16 + 4 * h);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] = f16_to_f32(sv[e]);
@@ -388,6 +388,26 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
     }
     return;
   }
+  if (a.epi.on) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (nt0 + t >= a.ntiles) continue;
+      const int n = (nt0 + t) * 16 + 4 * h;
+      float s[4];
+      col_scales(t, s);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = m0 + 16 * i + c;
+        if (m < a.M) {
+          const size_t at = (size_t)m * a.N + n;
+          const f4 v = epilogue4<DT>(
+              f4{acc[i][t][0] * s[0], acc[i][t][1] * s[1], acc[i][t][2] * s[2], acc[i][t][3] * s[3]}, a.epi, at, n);
+          *(u32x2*)(a.y + at) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     if (nt0 + t >= a.ntiles) continue;
@@ -415,7 +435,8 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
 // order: a fixed summation order for a given shape.
 template <int DT>
 __global__ __launch_bounds__(256) void ksplit_reduce_kernel(const float* __restrict__ part, int ksplit, int M, int N,
-                                                            int swiglu, int rows, uint16_t* __restrict__ y) {
+                                                            int swiglu, int rows, const EpilogueArgs epi,
+                                                            uint16_t* y) {
   __shared__ f4 red_g[256], red_u[256];
   const int ldy = swiglu ? N / 2 : N;
   const size_t quads = (size_t)M * ldy / 4;
@@ -449,6 +470,8 @@ __global__ __launch_bounds__(256) void ksplit_reduce_kernel(const float* __restr
   if (swiglu) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) g[e] = g[e] / (1.0f + expf(-g[e])) * u[e];
+  } else if (epi.on) {
+    g = epilogue4<DT>(g, epi, (size_t)m * ldy + j, j);
   }
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   *(u32x2*)(y + (size_t)m * ldy + j) = u32x2{pack2<DT>(g[0], g[1]), pack2<DT>(g[2], g[3])};
@@ -524,7 +547,7 @@ wq_status run_gemm(GemmArgs g, hipStream_t s) {
     while (rows < 8 && rows < g.ksplit && quads * rows < ((size_t)1 << 18)) rows *= 2;
     const size_t qw = 256 / rows;
     hipLaunchKernelGGL((ksplit_reduce_kernel<DT>), dim3((unsigned)((quads + qw - 1) / qw)), dim3(256), 0, s,
-                       (const float*)g.part, g.ksplit, g.M, g.N, g.swiglu, rows, g.y);
+                       (const float*)g.part, g.ksplit, g.M, g.N, g.swiglu, rows, g.epi, g.y);
   }
   return launch_status();
 }
@@ -552,6 +575,7 @@ wq_status WQ_CAT(launch_gemm_, WQ_VARIANT)(const ProductArgs& p) {
   g.ksplit = p.ksplit;
   g.part = (float*)p.part;
   g.ktps = L.ktiles;
+  g.epi = EpilogueArgs{p.epi.bias, p.epi.residual, p.epi.act, p.epi.on() ? 1 : 0};
   const int gpu = L.gsz >= 128 ? 1 : 128 / L.gsz;
   const bool epi = L.G == 1 && p.mode == SYM && D == F16;
   wq_status st = WQ_EINVAL;

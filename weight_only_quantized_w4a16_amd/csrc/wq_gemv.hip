@@ -50,6 +50,7 @@ struct GemvArgs {
   int M, N, K, nrec, upr, ktiles, waves, kt_per_wave;  // upr: 128-row units per metadata record
   int ldy;                // row stride of y (N, or N / 2 for a fused gate+up layer)
   int force_waves, force_pf;  // launch-shape overrides (0: automatic)
+  EpilogueArgs epi;       // plain layers: act(y + bias) + residual before the rounding
 };
 
 // Whether the product multiplies the dequantised weights themselves (the
@@ -565,7 +566,16 @@ __global__ __launch_bounds__((gemv_big_frames<BITS, TN, GPU, MR>() ? 512 : 1024)
     // standard: row 16 rb + 4 (l / 16) + e, col l % 16
     const int m = PK == 4 ? (l >> 4) : PK == 8 ? 2 * (l >> 4) + e : 16 * rb + 4 * (l >> 4) + e;
     const int n = (SWIGLU ? (int)blockIdx.x : nt0 + t) * 16 + (l & 15);
-    if (m < a.M) a.y[(size_t)m * a.ldy + n] = DT == F16 ? f32_to_f16(v) : f32_to_bf16(v);
+    if (m < a.M) {
+      if constexpr (!SWIGLU) {
+        if (a.epi.on) {
+          if (a.epi.bias) v += elem_to_f32<DT>(a.epi.bias[n]);
+          v = activate(v, a.epi.act);
+          if (a.epi.residual) v += elem_to_f32<DT>(a.epi.residual[(size_t)m * a.ldy + n]);
+        }
+      }
+      a.y[(size_t)m * a.ldy + n] = DT == F16 ? f32_to_f16(v) : f32_to_bf16(v);
+    }
   }
 }
 
@@ -690,6 +700,7 @@ wq_status pick_shape(GemvArgs g, hipStream_t s) {
       GemvArgs hi = g;
       hi.x += (size_t)16 * g.K;
       hi.y += (size_t)16 * g.ldy;
+      if (hi.epi.residual) hi.epi.residual += (size_t)16 * g.ldy;
       hi.M = g.M - 16;
       g.M = 16;
       const wq_status st = pick_standard<DT, BITS, MODE, GPU, SWIGLU, 1>(g, s);
@@ -745,6 +756,7 @@ wq_status WQ_CAT(launch_gemv_, WQ_VARIANT)(const ProductArgs& p) {
   g.waves = 1; g.kt_per_wave = 0;
   g.force_waves = p.waves; g.force_pf = p.pf;
   g.ldy = p.swiglu ? p.N / 2 : p.N;
+  g.epi = EpilogueArgs{p.epi.bias, p.epi.residual, p.epi.act, p.epi.on() ? 1 : 0};
   const int gpu = L.gsz >= 128 ? 1 : 128 / L.gsz;  // groups per 128-row unit
   wq_status st = WQ_EINVAL;
   sfor<7>([&](auto mi) {  // the ABI mode itself: fine zero-points keep their group
