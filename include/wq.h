@@ -347,7 +347,7 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  * ones lose bits).  The same call gives the same bits.
  */
 size_t wq_kv_workspace_bytes(int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim,
-                             int max_kv_len);
+                             int group, int max_kv_len);
 wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* cache, const int32_t* block_table,
                           const int32_t* kv_lens, const int32_t* cu_q, void* out, int64_t ld_out, int rows, int batch,
                           int max_pages, int num_pages, int page_size, int q_heads, int kv_heads, int head_dim,

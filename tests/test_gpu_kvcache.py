@@ -248,11 +248,11 @@ def test_attention_masks(wq, new, causal, window):
 def test_attention_long_context_in_parts(wq, D, G, dt):
     """Few rows over many keys: the keys are split over workgroups and joined."""
     P = _kv.Problem([5003, 700], [1, 1], 1, D, G, 64, dt, D)
-    assert wq.wq_kv_workspace_bytes(2, 2, False, 4, 1, D, 5003) > 0
+    assert wq.wq_kv_workspace_bytes(2, 2, False, 4, 1, D, G, 5003) > 0
     check_attention(wq, P, 4)
     check_attention(wq, P, 4, window=1500, max_kv=5003)
     P = _kv.Problem([2100, 64], [40, 64], 1, D, G, 64, dt, D)
-    assert wq.wq_kv_workspace_bytes(104, 2, True, 4, 1, D, 2100) > 0
+    assert wq.wq_kv_workspace_bytes(104, 2, True, 4, 1, D, G, 2100) > 0
     check_attention(wq, P, 4)
 
 
@@ -400,7 +400,7 @@ def test_streams_and_graph(wq):
     H, D, Hq, T = 2, 128, 8, 1300
     P = _kv.Problem([T, T - 300], [1, 1], H, D, 128, 16, F16, 51)
     table = P.table.cuda()
-    need = wq.wq_kv_workspace_bytes(2, 2, False, Hq, H, D, T)
+    need = wq.wq_kv_workspace_bytes(2, 2, False, Hq, H, D, 128, T)
     assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     start = [T - 6, T - 306]

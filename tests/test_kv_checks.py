@@ -89,7 +89,7 @@ def test_attention_refusals(L):
     assert attend_call(L, ld_q=1028) == 2
     assert attend_call(L, ld_out=512) == 1
     assert attend_call(L, rows=1 << 24, batch=1, q_heads=128, ld_q=1 << 20, ld_out=1 << 20, max_kv=0) == 2
-    need = L.wq_kv_workspace_bytes(2, 2, 0, 8, 4, 128, 100000)
+    need = L.wq_kv_workspace_bytes(2, 2, 0, 8, 4, 128, 128, 100000)
     assert need > 0
     assert attend_call(L, max_kv=100000) == 4                  # workspace missing, short, misaligned
     assert attend_call(L, max_kv=100000, ws=128, ws_bytes=need - 1) == 4
@@ -97,12 +97,12 @@ def test_attention_refusals(L):
 
 
 def test_workspace_bytes(L):
-    assert wq.wq_kv_workspace_bytes(1, 1, False, 32, 32, 128, 64) == 0         # one part
-    assert wq.wq_kv_workspace_bytes(4096, 64, False, 64, 8, 128, 100000) == 0  # enough workgroups
-    for bad in ((0, 1, 32, 32, 128), (3, 2, 32, 32, 128), (1, 1, 33, 32, 128), (1, 1, 32, 32, 100)):
-        assert wq.wq_kv_workspace_bytes(bad[0], bad[1], False, bad[2], bad[3], bad[4], 100000) == 0
+    assert wq.wq_kv_workspace_bytes(1, 1, False, 32, 32, 128, 128, 64) == 0         # one part
+    assert wq.wq_kv_workspace_bytes(4096, 64, False, 64, 8, 128, 128, 100000) == 0  # enough workgroups
+    for bad in ((0, 1, 32, 32, 128), (3, 2, 32, 32, 128), (1, 1, 33, 32, 128), (1, 1, 32, 32, 96)):
+        assert wq.wq_kv_workspace_bytes(bad[0], bad[1], False, bad[2], bad[3], bad[4], 64, 100000) == 0
     # parts x rows x heads x (sums, reference, weight)
-    one = wq.wq_kv_workspace_bytes(1, 1, False, 8, 8, 128, 1 << 20)
+    one = wq.wq_kv_workspace_bytes(1, 1, False, 8, 8, 128, 64, 1 << 20)
     assert one % (8 * (128 + 2) * 4) == 0 and 2 <= one // (8 * (128 + 2) * 4) <= 128
 
 

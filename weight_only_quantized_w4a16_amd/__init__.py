@@ -74,7 +74,7 @@ def lib() -> ctypes.CDLL:
         L.wq_kv_write.restype = I
         L.wq_kv_read.argtypes = [P, P, P, L64, L64, I, P, P, P] + [I] * 8 + [P]
         L.wq_kv_read.restype = I
-        L.wq_kv_workspace_bytes.argtypes = [I] * 7
+        L.wq_kv_workspace_bytes.argtypes = [I] * 8
         L.wq_kv_workspace_bytes.restype = Z
         L.wq_kv_attention.argtypes = [P, L64, I, P, P, P, P, P, L64] + [I] * 9 + [F, I, I, I, P, Z, P]
         L.wq_kv_attention.restype = I

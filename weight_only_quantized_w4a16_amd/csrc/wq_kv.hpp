@@ -138,18 +138,18 @@ struct KvPlan {
   int splits;     // parts of the keys
   int slots, tiles;
 };
-// Row tiles per wave of the row form, and whether the key form has a variant
-// of two: 16 output registers per lane for every 64 channels of a tile.
-constexpr int kv_rows_form_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
-constexpr bool kv_wide_keys_form(int head_dim) { return head_dim <= 128; }
+// Whether a wave may take two row tiles (they share every code it unpacks):
+// the sums of a tile take 16 registers per lane for every 64 channels, the
+// offsets 4 for every group, and 256 registers are to hold it all.
+constexpr bool kv_two_tiles(int head_dim, int group) { return head_dim <= 128 && head_dim / group <= 2; }
 
 inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv_heads, int head_dim,
-                      int64_t max_kv) {
+                      int group, int64_t max_kv) {
   KvPlan p;
   // packed rows (token, head) of a sequence, on average
   const int64_t per = ((int64_t)rows * heads_per_kv + batch - 1) / batch;
   p.rows_form = per > 32;
-  p.nq = p.rows_form ? kv_rows_form_tiles(head_dim) : per > 16 && kv_wide_keys_form(head_dim) ? 2 : 1;
+  p.nq = per > 16 && kv_two_tiles(head_dim, group) ? 2 : 1;
   const int bm = (p.rows_form ? 64 : 16) * p.nq;
   p.tiles = (int)((per + bm - 1) / bm);
   p.slots = ragged ? (int)((int64_t)rows * heads_per_kv / bm + batch) : p.tiles * batch;

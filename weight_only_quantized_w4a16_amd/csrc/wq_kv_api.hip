@@ -72,12 +72,15 @@ wq_status kv_rows(bool write, void* cache, const void* k, const void* v, int64_t
                         (uint16_t*)const_cast<void*>(v), ld_k, ld_v, (int)dt, head_dim, group, (hipStream_t)stream);
 }
 
-bool plan_of(KvPlan& p, int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim, int64_t max_kv) {
+bool plan_of(KvPlan& p, int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim, int group,
+             int64_t max_kv) {
   if (rows <= 0 || batch <= 0 || q_heads <= 0 || kv_heads <= 0 || max_kv < 0) return false;
   if (rows > (1 << 24) || batch > (1 << 20) || q_heads > 4096 || kv_heads > 1024 || max_kv > ((int64_t)1 << 30))
     return false;
-  if (q_heads % kv_heads != 0 || !kv_head_dim_ok(head_dim) || (!ragged && rows % batch != 0)) return false;
-  p = kv_plan(rows, batch, ragged != 0, q_heads / kv_heads, kv_heads, head_dim, max_kv);
+  if (q_heads % kv_heads != 0 || !kv_head_dim_ok(head_dim) || group <= 0 || !kv_group_ok(head_dim, group) ||
+      (!ragged && rows % batch != 0))
+    return false;
+  p = kv_plan(rows, batch, ragged != 0, q_heads / kv_heads, kv_heads, head_dim, group, max_kv);
   return true;
 }
 
@@ -107,9 +110,9 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
 }
 
 size_t wq_kv_workspace_bytes(int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim,
-                             int max_kv_len) {
+                             int group, int max_kv_len) {
   KvPlan p;
-  if (!plan_of(p, rows, batch, ragged, q_heads, kv_heads, head_dim, max_kv_len)) return 0;
+  if (!plan_of(p, rows, batch, ragged, q_heads, kv_heads, head_dim, group, max_kv_len)) return 0;
   return kv_part_bytes(p, rows, q_heads, head_dim) + kv_ml_bytes(p, rows, q_heads);
 }
 
@@ -134,7 +137,8 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
   if ((st = check_rows(q, ld_q, rows, q_heads * head_dim)) != WQ_OK) return st;
   if ((st = check_rows(out, ld_out, rows, q_heads * head_dim)) != WQ_OK) return st;
   KvPlan p;
-  if (!plan_of(p, rows, batch, cu_q != nullptr, q_heads, kv_heads, head_dim, max_kv_len)) return WQ_EUNSUPPORTED;
+  if (!plan_of(p, rows, batch, cu_q != nullptr, q_heads, kv_heads, head_dim, group, max_kv_len))
+    return WQ_EUNSUPPORTED;
   if ((int64_t)p.slots * p.splits * kv_heads >= ((int64_t)1 << 31) || (int64_t)rows * q_heads > ((int64_t)1 << 30))
     return WQ_EUNSUPPORTED;
   const size_t part = kv_part_bytes(p, rows, q_heads, head_dim), need = part + kv_ml_bytes(p, rows, q_heads);

@@ -4,11 +4,12 @@
 //     a_j = scale * sum_d q_d (lo_j + s_j c_jd)      (s, lo per group of channels)
 //     o_d = sum_j e^(a_j - m) (lo_j + s_j c_jd) / sum_j e^(a_j - m).
 // No value is dequantised: the codes themselves are the MFMA operands.  A code
-// in the low bits of an fp16 is the subnormal c 2^-24, which the matrix cores
-// multiply exactly, so eight codes become operands with four ANDs and three
-// shifts.  The steps follow in fp32: on the scores, sum q (lo + s c) =
-// lo (sum q) + s (sum q c) per group; on the outputs s_j goes into the
-// probability and sum_j p_j lo_j is one more running sum.
+// in the low bits of an fp16 is the subnormal c 2^-24 (four bits further up,
+// c 2^-20), which the matrix cores multiply exactly, so eight codes become
+// operands with four ANDs and one shift; the other operand carries the 2^-4 of
+// every second pair.  Steps and offsets follow per group: the scores are
+// s ((lo / s) sum q + sum q c), the first term being the accumulator's start;
+// on the outputs s_j goes into the probability.
 //
 // Layout of the work: rows are (token, head) pairs that share a kv head, 16 to
 // an MFMA tile, so the heads of a group share every code that is read.  A wave
@@ -21,9 +22,15 @@
 //
 // Numbers: q is scaled by a power of two per row so that its largest channel
 // lies in [2^13, 2^14) and converted to fp16 (exact for fp16 and bf16 inputs
-// but for channels 2^-27 below the largest).  p s is rounded to fp16 once; its
-// reference is held so that the largest lies near 2^14, so products 2^-28
-// smaller are still normal numbers.  Scores, maxima and sums are fp32.
+// but for channels 2^-23 below the largest).  P = p s is rounded to fp16 once;
+// its reference is held so that the largest lies near 2^14, so products 2^-24
+// smaller are still normal numbers.  The offsets are added as
+// sum P lo / s beside sum P c, from the same rounded P, so that a rounding of P
+// shows times v / s rather than times c: lo / s, as the sum of two fp16, is one
+// more operand tile of the second product (rows 0 and 1 of it).  fp16 outputs,
+// one row over 1037 keys: 0.39e-3 of the norm when the offsets were summed apart,
+// LATER now; the rounding of the output alone is 0.20e-3.  A group without a step
+// (all channels alike) takes |lo| for one.  Scores, maxima and sums are fp32.
 //
 // Two forms.  Few rows per sequence (decode): the four waves of a workgroup
 // take the blocks of 64 keys in turn and merge through LDS.  Many rows: each
@@ -42,20 +49,25 @@ namespace {
 constexpr float kNone = -1e30f;    // reference of a row that has seen no key
 constexpr float kSlack = 8.0f;     // log2 a score may exceed its row's reference by
 constexpr int kStepMin = -60;      // smallest exponent the value steps are referred to
-
-// Steps and offsets travel with the codes where they fit the registers (one or
-// two groups); with more groups they are read where they are used.
-constexpr int kMetaHeld = 2;
+constexpr float kStepZero = 0x1p-100f;  // smaller steps (bf16 only) count as none
 
 template <int D, int NG>
 struct KvBlock {  // one lane's share of a block of 64 keys
-  static constexpr int HELD = NG <= kMetaHeld ? NG : 0;
   uint32_t k[4][D / 32];
   u32x4 v[D / 32];
-  u32x4 km[HELD ? HELD : 1][4], vm[HELD ? HELD : 1][4];
-  const u32x4* meta;  // of this lane's 16 keys
-  int rec;            // their record, -1: none
+  uint32_t km[NG], vm[NG];  // step and offset of key c of this lane group's 16
 };
+
+// value of lane I of each row of 16 lanes (DPP row broadcast: an operand
+// modifier of the instruction that uses it)
+template <int I>
+__device__ inline uint32_t row_bcast_u(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + I, 0xf, 0xf, true);
+}
+template <int I>
+__device__ inline float row_bcast(float v) {
+  return __uint_as_float(row_bcast_u<I>(__float_as_uint(v)));
+}
 
 // W consecutive words, W = 2, 3, 4, 6 or 8
 template <int W>
@@ -83,17 +95,18 @@ __device__ inline void load_words(uint32_t (&dst)[W], const uint32_t* src) {
   }
 }
 
-// eight codes of a word as fp16 c 2^-24, in the order 0 4 1 5 2 6 3 7
+// eight codes of a word as fp16, in the order 0 4 | 1 5 | 2 6 | 3 7: c 2^-24 in
+// the first and third pair, c 2^-20 in the second and fourth
 __device__ inline u32x4 code_frag(uint32_t w) {
-  constexpr uint32_t m = 0x000F000Fu;
-  return u32x4{w & m, (w >> 4) & m, (w >> 8) & m, (w >> 12) & m};
+  const uint32_t v = w >> 8;
+  return u32x4{w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u};
 }
 
 template <int DT, int D, int NG, int NQ, bool ROWS>
-__global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
+__global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a) {
   constexpr int W = D / 32, DTL = D / 16, G = D / NG, REC = kv_record_bytes(D, NG);
   constexpr int BM = ROWS ? 64 * NQ : 16 * NQ;  // rows of a workgroup
-  constexpr int LDO = D + 4, HELD = KvBlock<D, NG>::HELD;
+  constexpr int LDO = D + 4;
   // the merge of the waves: references and sums, then outputs
   __shared__ __attribute__((aligned(16))) float lds[ROWS ? 4 : 4 * BM * (2 + LDO)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -122,9 +135,13 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
   if (tile < 0 || r0 >= nrows) return;  // the same for every wave of the workgroup
   const int w0 = ROWS ? r0 + wave * 16 * NQ : r0;
 
-  // rows of this lane, their limits and operands
+  // rows of this lane, their limits and operands; with more than
+  // four the operands stay in LDS (every lane its own, so no wave waits for another)
+  constexpr bool QLDS = NQ * W > 4;
+  __shared__ u32x4 qstage[QLDS ? (ROWS ? 4 : 1) * NQ * W * 64 : 1];
+  u32x4* qlds = qstage + (QLDS && ROWS ? wave * NQ * W * 64 : 0);
   float cq[NQ], qs[NQ][NG];
-  u32x4 qf[NQ][W];
+  u32x4 qf[QLDS ? 1 : NQ][W];
   int hi[NQ], lo[NQ];
   int hi_min = 0x7FFFFFFF, hi_max = 0, lo_min = 0x7FFFFFFF, lo_max = 0;
 #pragma unroll
@@ -169,6 +186,7 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
 #pragma unroll
     for (int kb = 0; kb < W; ++kb) {
       float v[8];
+      u32x4 row;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         v[2 * p] = act_lo<DT>(raw[kb][p]) * f;
@@ -176,10 +194,13 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
       }
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t w = pack2<F16>(v[p], v[p + 4]);  // the order of code_frag
-        qf[n][kb][p] = w;
-        qs[n][kb * 32 / G] += f16_to_f32((uint16_t)w) + f16_to_f32((uint16_t)(w >> 16));
+        const float f = p & 1 ? 0x1p-4f : 1.0f;  // the order and scale of code_frag
+        const uint32_t w = pack2<F16>(v[p] * f, v[p + 4] * f);
+        row[p] = w;
+        qs[n][kb * 32 / G] += (f16_to_f32((uint16_t)w) + f16_to_f32((uint16_t)(w >> 16))) * (p & 1 ? 0x1p4f : 1.0f);
       }
+      if constexpr (QLDS) qlds[(n * W + kb) * 64 + lane] = row;
+      else qf[n][kb] = row;
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -216,16 +237,18 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
   constexpr int stride = ROWS ? 1 : 4;
   const int nblk = begin < end ? (end - begin + stride - 1) / stride : 0;
 
-  f4 acc[NQ][DTL];
-  float ref[NQ], m[NQ], sum[NQ], lsum[NQ][NG];
-  int step_exp = kStepMin;  // the steps of the values seen are below 2^(step_exp + 6)
+  f4 acc[NQ][DTL], off[NQ][NG];
+  float ref[NQ], m[NQ], sum[NQ];
+  // the steps of the values seen are at most step_limit = 2^(step_exp + 6)
+  int step_exp = kStepMin;
+  float step_limit = __uint_as_float((uint32_t)(127 + 6 + kStepMin) << 23);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n] = kNone;
     ref[n] = kNone + kStepMin;
     sum[n] = 0.0f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) lsum[n][g] = 0.0f;
+    for (int g = 0; g < NG; ++g) off[n][g] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < DTL; ++t) acc[n][t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -236,88 +259,109 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
     const int blk = begin + (at + (lane >> 2)) * stride;
     return blk < end ? kv_record(a.seqs, b, blk * 4 + (lane & 3), kvh) : -1;
   };
-  auto load = [&](KvBlock<D, NG>& f, int recs, int t) __attribute__((always_inline)) {
-    const int rk = __shfl(recs, 4 * t + (c >> 2), 64), rv = __shfl(recs, 4 * t + h, 64);
-    // a block that is not there is read as record 0 and masked
-    const uint8_t* pk = a.cache + (size_t)(uint32_t)(rk < 0 ? 0 : rk) * REC;
-    const uint8_t* pv = a.cache + (size_t)(uint32_t)(rv < 0 ? 0 : rv) * REC;
-    f.rec = rv;
+  // The loads of the next block's keys follow this block's scores, those of its
+  // values this block's outputs: each into the registers just read, so a block
+  // is held once and its loads have most of a block's work to arrive in.
+  KvBlock<D, NG> f;
+  // blocks and records that are not there are read as record 0 and masked
+  auto record_at = [&](int rec) { return a.cache + (size_t)(uint32_t)(rec < 0 ? 0 : rec) * REC; };
+  auto load_keys = [&](int recs, int t) __attribute__((always_inline)) {
+    const uint8_t* pk = record_at(__shfl(recs, 4 * t + (c >> 2), 64));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j)
       load_words<W>(f.k[j], (const uint32_t*)pk + (4 * j + (c & 3)) * (4 * W) + h * W);
-    }
+    const uint8_t* pm = record_at(__shfl(recs, 4 * t + h, 64)) + 16 * D;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) f.km[g] = ((const uint32_t*)pm)[16 * g + c];
+  };
+  auto load_values = [&](int recs, int t) __attribute__((always_inline)) {
+    const uint8_t* pv = record_at(__shfl(recs, 4 * t + h, 64));
 #pragma unroll
     for (int p = 0; p < W; ++p) f.v[p] = ((const u32x4*)(pv + 8 * D))[p * 16 + c];
-    f.meta = (const u32x4*)(pv + 16 * D);
 #pragma unroll
-    for (int g = 0; g < HELD; ++g)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f.km[g][j] = f.meta[4 * g + j];
-        f.vm[g][j] = f.meta[4 * NG + 4 * g + j];
-      }
+    for (int g = 0; g < NG; ++g) f.vm[g] = ((const uint32_t*)(pv + 16 * D))[16 * (NG + g) + c];
   };
 
-  auto compute = [&](KvBlock<D, NG>& f, int blk) __attribute__((always_inline)) {
-    const int key0 = blk * 64;
-    const bool edge = key0 + 64 > hi_min || key0 < lo_max || __any(f.rec < 0);
-    const int kl = key0 + 16 * h;  // this lane's first key
-    auto key_meta = [&](int g, int j) __attribute__((always_inline)) {
-      if constexpr (HELD) return f.km[g][j];
-      else return f.meta[4 * g + j];
-    };
-    auto value_meta = [&](int g, int j) __attribute__((always_inline)) {
-      u32x4 v;
-      if constexpr (HELD) v = f.vm[g][j];
-      else v = f.meta[4 * NG + 4 * g + j];
-      if (edge) {  // keys that are not there count as zero whatever the memory holds
+  // which half of (hi, lo) pairs of two keys this lane's row of the offset
+  // operand takes: row 0 the first, row 1 the second (the other rows are not used)
+  const uint32_t offset_sel = c & 1 ? 0x07060302u : 0x05040100u;
+
+  // one block: rec is the record of this lane's 16 keys (-1: none); recs and t
+  // say where the next block is
+  auto compute = [&](int blk, int rec, int recs, int t) __attribute__((always_inline)) {
+    const int kl = blk * 64 + 16 * h;  // this lane's first key
+    // whether some key is hidden from some row (the same for the whole wave)
+    const bool edge = blk * 64 + 64 > hi_min || blk * 64 < lo_max || __any(rec < 0);
+    // step and offset / step of this lane's key
+    float ks[NG], kr[NG];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (f.rec < 0 || kl + 4 * j + i >= sq.len) v[i] = 0u;
-      }
-      return v;
-    };
+    for (int g = 0; g < NG; ++g) {
+      ks[g] = act_lo<DT>(f.km[g]);
+      kr[g] = act_hi<DT>(f.km[g]);
+      const bool flat = ks[g] < kStepZero;
+      ks[g] = flat ? 1.0f : ks[g];
+      kr[g] *= flat ? 1.0f : __builtin_amdgcn_rcpf(ks[g]);
+    }
     // scores: keys x rows
     f4 u[NQ][4];
+    if constexpr (QLDS) asm volatile("" ::: "memory");  // the row operands are read again, not kept
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int g = 0; g < NG; ++g) {
+      f4 d[NQ][4];
+      sfor<16>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        f4 d[NQ];
+        for (int n = 0; n < NQ; ++n) d[n][i / 4][i % 4] = row_bcast<i>(kr[g]) * qs[n][g];
+      });
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) d[n] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int kb = g * (G / 32); kb < (g + 1) * (G / 32); ++kb) {
+        u32x4 q[NQ];
 #pragma unroll
-        for (int kb = g * (G / 32); kb < (g + 1) * (G / 32); ++kb) {
+        for (int n = 0; n < NQ; ++n) {
+          if constexpr (QLDS) q[n] = qlds[(n * W + kb) * 64 + lane];
+          else q[n] = qf[n][kb];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
           const u32x4 kf = code_frag(f.k[j][kb]);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) d[n] = mfma16<F16>(kf, qf[n][kb], d[n]);
-        }
-        const u32x4 km = key_meta(g, j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = act_lo<DT>(km[i]), l = act_hi<DT>(km[i]);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            const float base = g == 0 ? l * qs[n][g] : __builtin_fmaf(l, qs[n][g], u[n][j][i]);
-            u[n][j][i] = __builtin_fmaf(s, d[n][i], base);
-          }
+          for (int n = 0; n < NQ; ++n) d[n][j] = mfma16<F16>(kf, q[n], d[n][j]);
         }
       }
+      sfor<16>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const float x = row_bcast<i>(ks[g]) * d[n][i / 4][i % 4];
+          u[n][i / 4][i % 4] = g == 0 ? x : u[n][i / 4][i % 4] + x;
+        }
+      });
     }
-    // largest value step of this lane's keys
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 sm = {0, 0};
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys(recs, t);
+    // step and offset / step of this lane's value
+    float vs[NG], smax = 0.0f;
+    uint32_t vr[NG];
+    bool nan_value = false;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 vm = value_meta(g, j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sm = __builtin_elementwise_max(sm, __builtin_bit_cast(u16x2, vm[i]));
-      }
-    if constexpr (!HELD) asm volatile("" ::: "memory");  // read again below rather than kept
-    const float smax = act_lo<DT>((uint32_t)sm[0]);
-    bool over = smax > ldexpf(1.0f, step_exp + 6);
+    for (int g = 0; g < NG; ++g) {
+      // values of keys that are not there count as zero whatever the memory holds
+      const uint32_t m = rec < 0 || kl + c >= sq.len ? 0u : f.vm[g];
+      const float l = act_hi<DT>(m);
+      float st = act_lo<DT>(m);
+      if (st < kStepZero) st = fabsf(l);  // NaN for a group of NaN
+      if (st < kStepZero) st = 0.0f;
+      // lo / s of the tokens with a factor 2^-4 in their probability as it is,
+      // of the others times 2^-4
+      float r = st > 0.0f ? l * __builtin_amdgcn_rcpf(st) : 0.0f;
+      r *= c & 1 ? 1.0f : 0x1p-4f;
+      const float r1 = f16_to_f32(f32_to_f16(r));
+      vr[g] = pack2<F16>(r1, r - r1);
+      nan_value |= st != st;
+      smax = fmaxf(smax, st);
+      vs[g] = c & 1 ? st * 0x1p-4f : st;
+    }
+    bool over = smax > step_limit;
     float top[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -327,7 +371,7 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = kl + 4 * j + i;
-            if (f.rec < 0 || key >= hi[n] || key < lo[n]) u[n][j][i] = -INFINITY;
+            if (rec < 0 || key >= hi[n] || key < lo[n]) u[n][j][i] = -INFINITY;
           }
       }
       float t = fmaxf(fmaxf(u[n][0][0], u[n][0][1]), fmaxf(u[n][0][2], u[n][0][3]));
@@ -339,12 +383,14 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
     }
     if (__any(over)) {
       // new references: sums so far are brought to them
-      float sx = fmaxf(smax, __shfl_xor(smax, 16, 64));
-      sx = fmaxf(sx, __shfl_xor(sx, 32, 64));
+      float sx = smax;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) sx = fmaxf(sx, __shfl_xor(sx, o, 64));
       int e = (int)((__float_as_uint(sx) >> 23) & 255) - 127 - 2;  // sx 2^-e in [4, 8)
-      if (e > 123) e = 123;
+      if (e > 120) e = 120;
       e = __builtin_amdgcn_readfirstlane(e);
       if (e > step_exp) step_exp = e;
+      step_limit = __uint_as_float((uint32_t)(127 + 6 + step_exp) << 23);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         float t = fmaxf(top[n], __shfl_xor(top[n], 16, 64));
@@ -355,79 +401,89 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
         ref[n] = nref;
         sum[n] *= al;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) lsum[n][g] *= al;
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) off[n][g][i] *= al;
 #pragma unroll
         for (int x = 0; x < DTL; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][x][i] *= al;
       }
     }
-    // probabilities, times the value step of each group, as operands: element
-    // 2 i of half hf is key 4 (2 hf) + i, element 2 i + 1 key 4 (2 hf + 1) + i
-    u32x4 pf[NQ][NG][2];
+    // probabilities (in the scores' registers)
+    const bool hidden_nan = edge && __any(nan_value);
+    uint32_t hide[NQ];  // bit 4 j + i: the key is hidden, where that matters below
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      f4 p[4];
+      hide[n] = 0;
+      if (hidden_nan)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) hide[n] |= u[n][i / 4][i % 4] == -INFINITY ? 1u << i : 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          p[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(u[n][j][i], cq[n], -ref[n]));
-          sum[n] += p[j][i];
+          u[n][j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(u[n][j][i], cq[n], -ref[n]));
+          sum[n] += u[n][j][i];
         }
+    }
+    // Group by group: times the value step as operands -- element 2 i of half
+    // hf is key 4 (2 hf) + i, element 2 i + 1 key 4 (2 hf + 1) + i -- and the
+    // outputs, transposed: channels x rows.
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
+    for (int g = 0; g < NG; ++g) {
+      u32x4 pf[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
         f4 ps[4];
+        sfor<16>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          ps[i / 4][i % 4] = row_bcast<i>(vs[g]) * u[n][i / 4][i % 4];
+        });
+        if (hidden_nan) {  // 0 NaN of a hidden key is 0
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 vm = value_meta(g, j);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float l = act_hi<DT>(vm[i]), s = act_lo<DT>(vm[i]);
-            if (edge) {  // a hidden key may hold anything
-              const int key = kl + 4 * j + i;
-              if (key >= hi[n] || key < lo[n]) l = s = 0.0f;
-            }
-            lsum[n][g] = __builtin_fmaf(p[j][i], l, lsum[n][g]);
-            ps[j][i] = p[j][i] * s;
-          }
+          for (int i = 0; i < 16; ++i) ps[i / 4][i % 4] = hide[n] >> i & 1 ? 0.0f : ps[i / 4][i % 4];
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pf[n][g][hf][i] = pack2<F16>(ps[2 * hf][i], ps[2 * hf + 1][i]);
+          for (int i = 0; i < 4; ++i) pf[n][hf][i] = pack2<F16>(ps[2 * hf][i], ps[2 * hf + 1][i]);
       }
-    }
-    // outputs, transposed: channels x rows
+      sfor<2>([&](auto hc) __attribute__((always_inline)) {
+        constexpr int hf = decltype(hc)::value;
+        u32x4 rf;
+        sfor<4>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          const uint32_t a0 = row_bcast_u<8 * hf + i>(vr[g]), a1 = row_bcast_u<8 * hf + 4 + i>(vr[g]);
+          rf[i] = __builtin_amdgcn_perm(a1, a0, offset_sel);
+        });
 #pragma unroll
-    for (int p = 0; p < W; ++p)
+        for (int n = 0; n < NQ; ++n) off[n][g] = mfma16<F16>(rf, pf[n][hf], off[n][g]);
+      });
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int t = 2 * p + o, g = 16 * t / G;
+      for (int t = g * (G / 16); t < (g + 1) * (G / 16); ++t)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const u32x4 vf = code_frag(f.v[p][2 * o + hf]);
+          const u32x4 vf = code_frag(f.v[t / 2][2 * (t % 2) + hf]);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) acc[n][t] = mfma16<F16>(vf, pf[n][g][hf], acc[n][t]);
+          for (int n = 0; n < NQ; ++n) acc[n][t] = mfma16<F16>(vf, pf[n][hf], acc[n][t]);
         }
-      }
+    }
   };
 
   if (nblk > 0) {
-    KvBlock<D, NG> f0, f1;
-    int recs = records(0), next = nblk > 16 ? records(16) : -1;
-    load(f0, recs, 0);
-    for (int t = 0; t < nblk; t += 2) {
-      // blocks past the last one load record 0 and are not computed
-      load(f1, recs, (t + 1) & 15);
-      compute(f0, begin + t * stride);
-      if (t + 1 >= nblk) break;
-      if (((t + 2) & 15) == 0) {
-        recs = next;
-        next = records(t + 18);
-      }
-      load(f0, recs, (t + 2) & 15);
-      compute(f1, begin + (t + 1) * stride);
+    int recs = records(0);
+    load_keys(recs, 0);
+    load_values(recs, 0);
+    int rec = __shfl(recs, h, 64);
+    for (int t = 0; t < nblk; ++t) {
+      // the next block (past the last one: record 0, loaded and not used)
+      const int next = (t + 1) & 15;
+      if (next == 0) recs = records(t + 1);
+      compute(begin + t * stride, rec, recs, next);
+      __builtin_amdgcn_sched_barrier(0);
+      load_values(recs, next);
+      rec = __shfl(recs, 4 * next + h, 64);
     }
   }
 
@@ -436,15 +492,13 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnArgs a) {
   for (int n = 0; n < NQ; ++n) {
     sum[n] += __shfl_xor(sum[n], 16, 64);
     sum[n] += __shfl_xor(sum[n], 32, 64);
+    float lsum[NG];  // rows 0 and 1 of the offset tile are with lane group 0
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      lsum[n][g] += __shfl_xor(lsum[n][g], 16, 64);
-      lsum[n][g] += __shfl_xor(lsum[n][g], 32, 64);
-    }
+    for (int g = 0; g < NG; ++g) lsum[g] = __shfl(off[n][g][0] + off[n][g][1], c, 64) * 0x1p4f;
 #pragma unroll
     for (int t = 0; t < DTL; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][t][i] = __builtin_fmaf(acc[n][t][i], 0x1p24f, lsum[n][16 * t / G]);
+      for (int i = 0; i < 4; ++i) acc[n][t][i] = __builtin_fmaf(acc[n][t][i], 0x1p24f, lsum[16 * t / G]);
   }
 
   // Store 4 channels of row r (of the sequence's packed rows): the output, or
@@ -593,9 +647,10 @@ wq_status pick(const KvAttnArgs& a, int G, const KvPlan& p) {
     if constexpr (WQ_HEAD_DIM % GG == 0) {
       if (GG != G) return;
       constexpr int NG = WQ_HEAD_DIM / GG;
-      if (p.rows_form) st = run<DT, NG, kv_rows_form_tiles(WQ_HEAD_DIM), true>(a);
+      constexpr int NQ = kv_two_tiles(WQ_HEAD_DIM, GG) ? 2 : 1;
+      if (p.rows_form) st = run<DT, NG, NQ, true>(a);
       else if (p.nq == 1) st = run<DT, NG, 1, false>(a);
-      else if constexpr (kv_wide_keys_form(WQ_HEAD_DIM)) st = run<DT, NG, 2, false>(a);
+      else st = run<DT, NG, NQ, false>(a);
     }
   };
   go(std::integral_constant<int, 32>{});

@@ -139,8 +139,9 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
 
 
 def wq_kv_workspace_bytes(rows: int, batch: int, ragged: bool, q_heads: int, kv_heads: int, head_dim: int,
-                          max_kv_len: int) -> int:
-    return int(lib().wq_kv_workspace_bytes(rows, batch, int(bool(ragged)), q_heads, kv_heads, head_dim, max_kv_len))
+                          group: int, max_kv_len: int) -> int:
+    return int(lib().wq_kv_workspace_bytes(rows, batch, int(bool(ragged)), q_heads, kv_heads, head_dim, group,
+                                           max_kv_len))
 
 
 def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -168,7 +169,8 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _need(isinstance(max_kv_len, int) and max_kv_len >= 0, "max_kv_len must be a count")
     if out is not None:
         _check_rows(out, "out", cache, q_heads, rows)
-    need = wq_kv_workspace_bytes(rows, batch, cu_q is not None, q_heads, cache.kv_heads, cache.head_dim, max_kv_len)
+    need = wq_kv_workspace_bytes(rows, batch, cu_q is not None, q_heads, cache.kv_heads, cache.head_dim,
+                                 cache.group, max_kv_len)
     if ws is not None and need:
         _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == q.device,
               "ws must be a contiguous tensor on the device of q")
