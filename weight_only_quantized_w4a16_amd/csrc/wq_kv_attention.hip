@@ -308,11 +308,16 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f4 d[NQ][4];
-      sfor<16>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) d[n][i / 4][i % 4] = row_bcast<i>(kr[g]) * qs[n][g];
-      });
+      for (int n = 0; n < NQ; ++n) {
+        // a copy for every tile: the broadcasts then stay operand modifiers
+        float r = kr[g];
+        if (NQ > 1) asm volatile("" : "+v"(r));
+        sfor<16>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          d[n][i / 4][i % 4] = row_bcast<i>(r) * qs[n][g];
+        });
+      }
 #pragma unroll
       for (int kb = g * (G / 32); kb < (g + 1) * (G / 32); ++kb) {
         u32x4 q[NQ];
@@ -366,13 +371,15 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       if (edge) {
+        // the key's limits relative to this lane's first key; opaque, or the
+        // comparisons are made for every block and only used for these
+        int a0 = rec < 0 ? 16 : lo[n] - kl, a1 = hi[n] - kl;
+        asm volatile("" : "+v"(a0), "+v"(a1));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = kl + 4 * j + i;
-            if (rec < 0 || key >= hi[n] || key < lo[n]) u[n][j][i] = -INFINITY;
-          }
+          for (int i = 0; i < 4; ++i)
+            if (4 * j + i >= a1 || 4 * j + i < a0) u[n][j][i] = -INFINITY;
       }
       float t = fmaxf(fmaxf(u[n][0][0], u[n][0][1]), fmaxf(u[n][0][2], u[n][0][3]));
 #pragma unroll
@@ -416,9 +423,12 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       hide[n] = 0;
-      if (hidden_nan)
+      if (hidden_nan) {
+        float none = -INFINITY;
+        asm volatile("" : "+v"(none));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) hide[n] |= u[n][i / 4][i % 4] == -INFINITY ? 1u << i : 0u;
+        for (int i = 0; i < 16; ++i) hide[n] |= u[n][i / 4][i % 4] == none ? 1u << i : 0u;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -589,42 +599,67 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
   }
 }
 
-// Joins the parts of the keys: one wave per (row, head), channels over lanes,
-// parts in order.
+// Joins the parts of the keys: one workgroup per (row, head), as many parts at
+// a time as it has rows of D / 4 threads, the parts of a thread and then the
+// threads of a channel in order.  (64 parts of 64 rows, D = 128: 50 us with one
+// wave that took the parts one after the other, LATER.)
+constexpr int kMaxSplits = 128;
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttnArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t all = (int64_t)a.seqs.rows * a.q_heads;
-  if (item >= all) return;
+  constexpr int VL = D / 4;
+  __shared__ float weight[kMaxSplits];
+  __shared__ f4 red[256];
+  const int64_t item = blockIdx.x, all = (int64_t)a.seqs.rows * a.q_heads;
   const int64_t row = item / a.q_heads;
   const int head = (int)(item - row * a.q_heads);
   // rows before the first or behind the last sequence belong to nobody
   if (a.seqs.cu_q && (row < kv_row_offset(a.seqs, 0) || row >= kv_row_offset(a.seqs, a.seqs.batch))) return;
-  float top = kNone * 2.0f;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_ml[((int64_t)s * all + item) * 2]);
-  float total = 0.0f;
-  constexpr int V = (D + 63) / 64;
-  float v[V];
+  // every wave: weight of each part against the largest reference
+  const int lane = threadIdx.x & 63;
+  float r[2] = {kNone * 2.0f, kNone * 2.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = a.part_ml[((int64_t)s * all + item) * 2 + 1];
-    if (w == 0.0f) continue;  // a part without keys (NaN goes on)
-    const float al = __builtin_amdgcn_exp2f(a.part_ml[((int64_t)s * all + item) * 2] - top);
-    total += w * al;
-    const float* p = a.part + ((int64_t)s * all + item) * D;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 64 * i < D) v[i] = __builtin_fmaf(p[lane + 64 * i], al, v[i]);
-  }
-  const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane + 64 * i < D) {
-      const float o = v[i] * inv;
-      a.out[row * a.ldo + (int64_t)head * D + lane + 64 * i] = DT == F16 ? f32_to_f16(o) : f32_to_bf16(o);
+  for (int k = 0; k < 2; ++k) {
+    const int s = lane + 64 * k;
+    if (s < a.splits) {
+      const float* ml = a.part_ml + ((int64_t)s * all + item) * 2;
+      r[k] = ml[0];
+      w[k] = ml[1];
     }
+  }
+  float top = fmaxf(r[0], r[1]);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  float total = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float al = __builtin_amdgcn_exp2f(r[k] - top);
+    // a part that saw no key holds nothing (NaN goes on)
+    if (threadIdx.x < 64) weight[lane + 64 * k] = w[k] == 0.0f ? 0.0f : al;
+    total += w[k] * al;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o, 64);
+  __syncthreads();
+  const int par = blockDim.x / VL, x = threadIdx.x % VL, y = threadIdx.x / VL;
+  f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (y < par) {
+    const float* p = a.part + item * D + 4 * x;
+#pragma unroll 4
+    for (int s = y; s < a.splits; s += par) {
+      const float al = weight[s];
+      const f4 t = *(const f4*)(p + (int64_t)s * all * D);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = al == 0.0f ? v[i] : __builtin_fmaf(t[i], al, v[i]);
+    }
+  }
+  red[threadIdx.x] = v;
+  __syncthreads();
+  if (y != 0) return;
+  for (int k = 1; k < par; ++k) v += red[k * VL + x];
+  const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  *(u32x2*)(a.out + row * a.ldo + (int64_t)head * D + 4 * x) =
+      u32x2{pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
 }
 
 template <int DT, int NG, int NQ, bool ROWS>
@@ -635,7 +670,8 @@ wq_status run(const KvAttnArgs& a) {
   wq_status st = launch_status();
   if (st != WQ_OK || a.splits == 1) return st;
   const int64_t items = (int64_t)a.seqs.rows * a.q_heads;
-  hipLaunchKernelGGL((kv_join_kernel<DT, D>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, a.stream, a);
+  const int threads = a.splits * (D / 4) > 128 ? 256 : 128;  // at least one part at a time (D / 4 <= 64)
+  hipLaunchKernelGGL((kv_join_kernel<DT, D>), dim3((unsigned)items), dim3(threads), 0, a.stream, a);
   return launch_status();
 }
 
