@@ -81,34 +81,35 @@ __device__ inline uint32_t pack2(float lo, float hi) {
 // v / (1 + e^-(a v + b v^3)), so one formula with two coefficients (times
 // log2 e) serves both; for v far below zero the exponential is infinite and the
 // quotient -0.  The hardware's exponential and reciprocal (1 ulp each) take a
-// third of the instructions of expf and a division: LATER.
+// third of the instructions of expf and a division (2048 x 12288 outputs of a
+// 4096-deep product with bias and GELU: 230 us with those, 193 with these).
 struct EpilogueArgs {
   const uint16_t *bias, *residual;
   int act;
   int on;
 };
+__device__ inline bool smooth_act(int act) { return act == WQ_ACT_SILU || act == WQ_ACT_GELU; }
+template <bool SMOOTH>
 __device__ inline float activate(float v, int act) {
-  if (act == WQ_ACT_RELU) return v < 0.0f ? 0.0f : v;
-  if (act != WQ_ACT_NONE) {
+  if constexpr (SMOOTH) {
     float t = -1.4426950408889634f;
     if (act == WQ_ACT_GELU) t = __builtin_fmaf(-0.1029432395800235f, v * v, -2.302208198144325f);
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * t));
+  } else {
+    const float floor = act == WQ_ACT_RELU ? 0.0f : -INFINITY;  // NaN stays
+    return v < floor ? floor : v;
   }
-  return v;
 }
 template <int DT>
 __device__ inline float elem_to_f32(uint16_t h) {
   return DT == F16 ? f16_to_f32(h) : bf16_to_f32(h);
 }
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
-// four consecutive outputs of row m, columns n .. n + 3 (n a multiple of 4)
-template <int DT>
-__device__ inline f4 epilogue4(f4 v, const EpilogueArgs& e, size_t at, int n) {
-  u16x4 b = {0, 0, 0, 0}, r = {0, 0, 0, 0};
-  if (e.bias) b = *(const u16x4*)(e.bias + n);
-  if (e.residual) r = *(const u16x4*)(e.residual + at);
+template <int DT, bool SMOOTH>
+__device__ inline f4 epilogue4(f4 v, u16x4 bias, u16x4 residual, int act) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = activate(v[i] + elem_to_f32<DT>(b[i]), e.act) + elem_to_f32<DT>(r[i]);
+  for (int i = 0; i < 4; ++i)
+    v[i] = activate<SMOOTH>(v[i] + elem_to_f32<DT>(bias[i]), act) + elem_to_f32<DT>(residual[i]);
   return v;
 }
 

@@ -389,23 +389,48 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
     return;
   }
   if (a.epi.on) {
+    // Everything to be added is loaded before anything is stored (the residual
+    // may be y, so no load could move above a store): the registers of the
+    // products' operands are free by now.
+    u16x4 bias[NT], res[NT][MT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (nt0 + t >= a.ntiles) continue;
-      const int n = (nt0 + t) * 16 + 4 * h;
-      float s[4];
-      col_scales(t, s);
+      bias[t] = u16x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = m0 + 16 * i + c;
-        if (m < a.M) {
-          const size_t at = (size_t)m * a.N + n;
-          const f4 v = epilogue4<DT>(
-              f4{acc[i][t][0] * s[0], acc[i][t][1] * s[1], acc[i][t][2] * s[2], acc[i][t][3] * s[3]}, a.epi, at, n);
-          *(u32x2*)(a.y + at) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      for (int i = 0; i < MT; ++i) res[t][i] = u16x4{0, 0, 0, 0};
+    }
+    if (a.epi.bias) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (nt0 + t < a.ntiles) bias[t] = *(const u16x4*)(a.epi.bias + (nt0 + t) * 16 + 4 * h);
+    }
+    if (a.epi.residual) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          if (nt0 + t < a.ntiles && m0 + 16 * i + c < a.M)
+            res[t][i] = *(const u16x4*)(a.epi.residual + (size_t)(m0 + 16 * i + c) * a.N + (nt0 + t) * 16 + 4 * h);
+    }
+    auto finish = [&](auto smooth) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (nt0 + t >= a.ntiles) continue;
+        float s[4];
+        col_scales(t, s);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int m = m0 + 16 * i + c;
+          const f4 v = epilogue4<DT, decltype(smooth)::value>(
+              f4{acc[i][t][0] * s[0], acc[i][t][1] * s[1], acc[i][t][2] * s[2], acc[i][t][3] * s[3]}, bias[t],
+              res[t][i], a.epi.act);
+          if (m < a.M)
+            *(u32x2*)(a.y + (size_t)m * a.N + (nt0 + t) * 16 + 4 * h) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
         }
       }
-    }
+    };
+    if (smooth_act(a.epi.act)) finish(std::true_type{});
+    else finish(std::false_type{});
     return;
   }
 #pragma unroll
@@ -471,7 +496,10 @@ __global__ __launch_bounds__(256) void ksplit_reduce_kernel(const float* __restr
 #pragma unroll
     for (int e = 0; e < 4; ++e) g[e] = g[e] / (1.0f + expf(-g[e])) * u[e];
   } else if (epi.on) {
-    g = epilogue4<DT>(g, epi, (size_t)m * ldy + j, j);
+    u16x4 b = {0, 0, 0, 0}, r = {0, 0, 0, 0};
+    if (epi.bias) b = *(const u16x4*)(epi.bias + j);
+    if (epi.residual) r = *(const u16x4*)(epi.residual + (size_t)m * ldy + j);
+    g = smooth_act(epi.act) ? epilogue4<DT, true>(g, b, r, epi.act) : epilogue4<DT, false>(g, b, r, epi.act);
   }
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   *(u32x2*)(y + (size_t)m * ldy + j) = u32x2{pack2<DT>(g[0], g[1]), pack2<DT>(g[2], g[3])};

@@ -570,7 +570,7 @@ __global__ __launch_bounds__((gemv_big_frames<BITS, TN, GPU, MR>() ? 512 : 1024)
       if constexpr (!SWIGLU) {
         if (a.epi.on) {
           if (a.epi.bias) v += elem_to_f32<DT>(a.epi.bias[n]);
-          v = activate(v, a.epi.act);
+          v = smooth_act(a.epi.act) ? activate<true>(v, a.epi.act) : activate<false>(v, a.epi.act);
           if (a.epi.residual) v += elem_to_f32<DT>(a.epi.residual[(size_t)m * a.ldy + n]);
         }
       }

@@ -131,10 +131,12 @@ struct KvAttnArgs {
   hipStream_t stream;
 };
 
+constexpr int kKvMaxSplits = 128;
 // Launch shape of an attention call: a function of the sizes the host knows.
 struct KvPlan {
   int rows_form;  // each wave its own rows (else the waves take the keys in turn)
   int nq;         // tiles of 16 rows per wave
+  int nw;         // waves of a workgroup
   int splits;     // parts of the keys
   int slots, tiles;
 };
@@ -142,6 +144,11 @@ struct KvPlan {
 // the sums of a tile take 16 registers per lane for every 64 channels, the
 // offsets 4 for every group, and 256 registers are to hold it all.
 constexpr bool kv_two_tiles(int head_dim, int group) { return head_dim <= 128 && head_dim / group <= 2; }
+// Waves per SIMD the registers of the one-tile key form leave room for, that is
+// workgroups of four waves per CU.
+constexpr int kv_key_waves(int head_dim, int group) {
+  return head_dim == 64 || (head_dim == 128 && group == 128) ? 3 : 2;
+}
 
 inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv_heads, int head_dim,
                       int group, int64_t max_kv) {
@@ -153,14 +160,28 @@ inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv
   const int bm = (p.rows_form ? 64 : 16) * p.nq;
   p.tiles = (int)((per + bm - 1) / bm);
   p.slots = ragged ? (int)((int64_t)rows * heads_per_kv / bm + batch) : p.tiles * batch;
-  // workgroups of four waves: about two to a CU; a part has at least two
-  // rounds of blocks of 64 keys
+  // Parts: as many as leave all workgroups resident at once (a few more would
+  // wait for a second round: one row of 64 heads over 131071 keys, group 64, two
+  // to a CU: 33 us with 512 workgroups, 38 with 768; 48 rows over up to 8000,
+  // three to a CU: 57.8 us with 384, 53.9 with 768, 57.6 with 1920), each of at
+  // least one round of blocks of 64 keys for the key form (a row over 1037 keys,
+  // 32 heads: 10.0 us in 5 parts, 11.7 in 2), four blocks for the row form.
   const int64_t wgs = (int64_t)p.slots * kv_heads;
-  const int64_t rounds = (max_kv + (p.rows_form ? 63 : 255)) / (p.rows_form ? 64 : 256);
-  int64_t s = wgs >= 512 ? 1 : 512 / wgs;
-  if (s > rounds / 2) s = rounds / 2;
-  if (s > 128) s = 128;
+  const int64_t room = 256 * (p.nq == 1 && !p.rows_form ? kv_key_waves(head_dim, group) : 2);
+  const int64_t rounds = p.rows_form ? max_kv / 256 : (max_kv + 255) / 256;
+  int64_t s = wgs >= room ? 1 : room / wgs;
+  if (s > rounds) s = rounds;
+  if (s > kKvMaxSplits) s = kKvMaxSplits;
   p.splits = s < 1 ? 1 : (int)s;
+  p.nw = 4;
+  // Short contexts of few rows take one workgroup of eight waves instead of
+  // parts and their join: over 1037 keys 10.3 us on the GPU against 10.0, and
+  // 10.7 against 14.7 for a call that is not captured (one launch, no
+  // workspace); over 2000 keys 13.1 against 10.2.
+  if (!p.rows_form && p.nq == 1 && p.splits > 1 && max_kv <= 1280) {
+    p.nw = 8;
+    p.splits = 1;
+  }
   return p;
 }
 // Workspace: sums of every part, then (reference, weight) pairs.

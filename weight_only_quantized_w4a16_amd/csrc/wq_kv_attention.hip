@@ -32,7 +32,7 @@
 // LATER now; the rounding of the output alone is 0.20e-3.  A group without a step
 // (all channels alike) takes |lo| for one.  Scores, maxima and sums are fp32.
 //
-// Two forms.  Few rows per sequence (decode): the four waves of a workgroup
+// Two forms.  Few rows per sequence (decode): the waves of a workgroup
 // take the blocks of 64 keys in turn and merge through LDS.  Many rows: each
 // wave has its own rows and all read the same codes through the L1.  Where the
 // rows do not fill the GPU the keys are split over workgroups as well, and a
@@ -102,13 +102,15 @@ __device__ inline u32x4 code_frag(uint32_t w) {
   return u32x4{w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u};
 }
 
-template <int DT, int D, int NG, int NQ, bool ROWS>
-__global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a) {
+// NW: waves of a workgroup.
+template <int DT, int D, int NG, int NQ, bool ROWS, int NW>
+__global__ __launch_bounds__(64 * NW, NQ == 1 && !ROWS && NW == 4 ? kv_key_waves(D, D / NG) : 2)
+void kv_attention_kernel(const KvAttnArgs a) {
   constexpr int W = D / 32, DTL = D / 16, G = D / NG, REC = kv_record_bytes(D, NG);
-  constexpr int BM = ROWS ? 64 * NQ : 16 * NQ;  // rows of a workgroup
+  constexpr int BM = ROWS ? 16 * NW * NQ : 16 * NQ;  // rows of a workgroup
   constexpr int LDO = D + 4;
   // the merge of the waves: references and sums, then outputs
-  __shared__ __attribute__((aligned(16))) float lds[ROWS ? 4 : 4 * BM * (2 + LDO)];
+  __shared__ __attribute__((aligned(16))) float lds[ROWS ? 4 : NW * BM * (2 + LDO)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, h = lane >> 4;
 
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
   // rows of this lane, their limits and operands; with more than
   // four the operands stay in LDS (every lane its own, so no wave waits for another)
   constexpr bool QLDS = NQ * W > 4;
-  __shared__ u32x4 qstage[QLDS ? (ROWS ? 4 : 1) * NQ * W * 64 : 1];
+  __shared__ u32x4 qstage[QLDS ? (ROWS ? NW : 1) * NQ * W * 64 : 1];
   u32x4* qlds = qstage + (QLDS && ROWS ? wave * NQ * W * 64 : 0);
   float cq[NQ], qs[NQ][NG];
   u32x4 qf[QLDS ? 1 : NQ][W];
@@ -227,14 +229,14 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
     const int first = lo_min >> 6, last = (hi_max + 63) >> 6;
     // parts of whole rounds over the workgroup's waves; a wave's rows alone
     // decide its range, so the parts of the row form may differ between waves
-    const int round = ROWS ? 1 : 4;
+    const int round = ROWS ? 1 : NW;
     const int rounds = (last - first + round - 1) / round;
     const int per = (rounds + a.splits - 1) / a.splits * round;
     begin = first + split * per;
     end = begin + per < last ? begin + per : last;
     if (!ROWS) begin += wave;
   }
-  constexpr int stride = ROWS ? 1 : 4;
+  constexpr int stride = ROWS ? 1 : NW;
   const int nblk = begin < end ? (end - begin + stride - 1) / stride : 0;
 
   f4 acc[NQ][DTL], off[NQ][NG];
@@ -259,13 +261,9 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
     const int blk = begin + (at + (lane >> 2)) * stride;
     return blk < end ? kv_record(a.seqs, b, blk * 4 + (lane & 3), kvh) : -1;
   };
-  // The loads of the next block's keys follow this block's scores, those of its
-  // values this block's outputs: each into the registers just read, so a block
-  // is held once and its loads have most of a block's work to arrive in.
-  KvBlock<D, NG> f;
   // blocks and records that are not there are read as record 0 and masked
   auto record_at = [&](int rec) { return a.cache + (size_t)(uint32_t)(rec < 0 ? 0 : rec) * REC; };
-  auto load_keys = [&](int recs, int t) __attribute__((always_inline)) {
+  auto load_keys = [&](KvBlock<D, NG>& f, int recs, int t) __attribute__((always_inline)) {
     const uint8_t* pk = record_at(__shfl(recs, 4 * t + (c >> 2), 64));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -274,7 +272,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
 #pragma unroll
     for (int g = 0; g < NG; ++g) f.km[g] = ((const uint32_t*)pm)[16 * g + c];
   };
-  auto load_values = [&](int recs, int t) __attribute__((always_inline)) {
+  auto load_values = [&](KvBlock<D, NG>& f, int recs, int t) __attribute__((always_inline)) {
     const uint8_t* pv = record_at(__shfl(recs, 4 * t + h, 64));
 #pragma unroll
     for (int p = 0; p < W; ++p) f.v[p] = ((const u32x4*)(pv + 8 * D))[p * 16 + c];
@@ -286,9 +284,9 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
   // operand takes: row 0 the first, row 1 the second (the other rows are not used)
   const uint32_t offset_sel = c & 1 ? 0x07060302u : 0x05040100u;
 
-  // one block: rec is the record of this lane's 16 keys (-1: none); recs and t
-  // say where the next block is
-  auto compute = [&](int blk, int rec, int recs, int t) __attribute__((always_inline)) {
+  // one block: rec is the record of this lane's 16 keys (-1: none); `scored` is
+  // called when its keys are not needed any more
+  auto compute = [&](KvBlock<D, NG>& f, int blk, int rec, auto scored) __attribute__((always_inline)) {
     const int kl = blk * 64 + 16 * h;  // this lane's first key
     // whether some key is hidden from some row (the same for the whole wave)
     const bool edge = blk * 64 + 64 > hi_min || blk * 64 < lo_max || __any(rec < 0);
@@ -342,8 +340,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
         }
       });
     }
-    __builtin_amdgcn_sched_barrier(0);
-    load_keys(recs, t);
+    scored();
     // step and offset / step of this lane's value
     float vs[NG], smax = 0.0f;
     uint32_t vr[NG];
@@ -482,18 +479,27 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
   };
 
   if (nblk > 0) {
-    int recs = records(0);
-    load_keys(recs, 0);
-    load_values(recs, 0);
-    int rec = __shfl(recs, h, 64);
+    // The loads of the next block's keys follow this block's scores, those of
+    // its values this block's outputs: each into the registers just read, so a
+    // block is held once and its loads have most of a block's work to arrive in.
+    // (With one tile, loading a whole block ahead takes 42 registers more and
+    // gains nothing: 8 waves on a CU, 20.5 us over 4000 keys against 19.9.)
+    auto rec_at = [&](int recs, int t) { return __shfl(recs, 4 * t + h, 64); };
+    KvBlock<D, NG> f;
+    int recs = records(0), rec = rec_at(recs, 0);
+    load_keys(f, recs, 0);
+    load_values(f, recs, 0);
     for (int t = 0; t < nblk; ++t) {
       // the next block (past the last one: record 0, loaded and not used)
       const int next = (t + 1) & 15;
       if (next == 0) recs = records(t + 1);
-      compute(begin + t * stride, rec, recs, next);
+      compute(f, begin + t * stride, rec, [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys(f, recs, next);
+      });
       __builtin_amdgcn_sched_barrier(0);
-      load_values(recs, next);
-      rec = __shfl(recs, 4 * next + h, 64);
+      load_values(f, recs, next);
+      rec = rec_at(recs, next);
     }
   }
 
@@ -549,10 +555,10 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
       if (a.splits > 1 && h == 0) store_ml(row, head, ref[n], sum[n]);
     }
   } else {
-    // merge the four waves: [wave][row] references and sums, then sums scaled
+    // merge the waves: [wave][row] references and sums, then sums scaled
     // to the largest reference
-    float* ml = lds;                      // [4][BM][2]
-    float* od = lds + 4 * BM * 2;         // [4][BM][LDO]
+    float* ml = lds;                // [NW][BM][2]
+    float* od = lds + NW * BM * 2;  // [NW][BM][LDO]
     if (h == 0) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -566,7 +572,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
       const int x = 16 * n + c;
       float top = ml[x * 2];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) top = fmaxf(top, ml[(w * BM + x) * 2]);
+      for (int w = 1; w < NW; ++w) top = fmaxf(top, ml[(w * BM + x) * 2]);
       const float al = __builtin_amdgcn_exp2f(ref[n] - top);
 #pragma unroll
       for (int t = 0; t < DTL; ++t) {
@@ -577,16 +583,16 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < BM * (D / 4); i += 256) {
+    for (int i = threadIdx.x; i < BM * (D / 4); i += 64 * NW) {
       const int x = i / (D / 4), d = 4 * (i % (D / 4));
       if (r0 + x >= nrows) continue;
       float top = ml[x * 2];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) top = fmaxf(top, ml[(w * BM + x) * 2]);
+      for (int w = 1; w < NW; ++w) top = fmaxf(top, ml[(w * BM + x) * 2]);
       float total = 0.0f;
       f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < NW; ++w) {
         total += ml[(w * BM + x) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(w * BM + x) * 2] - top);
         v += *(const f4*)(od + (w * BM + x) * LDO + d);
       }
@@ -603,11 +609,10 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const KvAttnArgs a
 // a time as it has rows of D / 4 threads, the parts of a thread and then the
 // threads of a channel in order.  (64 parts of 64 rows, D = 128: 50 us with one
 // wave that took the parts one after the other, LATER.)
-constexpr int kMaxSplits = 128;
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttnArgs a) {
   constexpr int VL = D / 4;
-  __shared__ float weight[kMaxSplits];
+  __shared__ float weight[kKvMaxSplits];
   __shared__ f4 red[256];
   const int64_t item = blockIdx.x, all = (int64_t)a.seqs.rows * a.q_heads;
   const int64_t row = item / a.q_heads;
@@ -662,11 +667,11 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttnArgs a) {
       u32x2{pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
 }
 
-template <int DT, int NG, int NQ, bool ROWS>
+template <int DT, int NG, int NQ, bool ROWS, int NW = 4>
 wq_status run(const KvAttnArgs& a) {
   constexpr int D = WQ_HEAD_DIM;
   const int64_t grid = (int64_t)a.slots * a.splits * a.seqs.kv_heads;
-  hipLaunchKernelGGL((kv_attention_kernel<DT, D, NG, NQ, ROWS>), dim3((unsigned)grid), dim3(256), 0, a.stream, a);
+  hipLaunchKernelGGL((kv_attention_kernel<DT, D, NG, NQ, ROWS, NW>), dim3((unsigned)grid), dim3(64 * NW), 0, a.stream, a);
   wq_status st = launch_status();
   if (st != WQ_OK || a.splits == 1) return st;
   const int64_t items = (int64_t)a.seqs.rows * a.q_heads;
@@ -685,6 +690,7 @@ wq_status pick(const KvAttnArgs& a, int G, const KvPlan& p) {
       constexpr int NG = WQ_HEAD_DIM / GG;
       constexpr int NQ = kv_two_tiles(WQ_HEAD_DIM, GG) ? 2 : 1;
       if (p.rows_form) st = run<DT, NG, NQ, true>(a);
+      else if (p.nw == 8) st = run<DT, NG, 1, false, 8>(a);
       else if (p.nq == 1) st = run<DT, NG, 1, false>(a);
       else st = run<DT, NG, NQ, false>(a);
     }
