@@ -104,6 +104,15 @@ def _stream(stream, dev: torch.device) -> int:
     return stream.cuda_stream
 
 
+def _used_on(stream, *tensors):
+    """Tensors this package allocates come from the current stream's memory.  Work given to another stream must keep
+    them from being handed out again before it is done with them."""
+    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(stream.device_index):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check(fn: str, rc: int):
     if rc != 0:
         raise WQError(fn, rc)
@@ -301,15 +310,17 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
         _need(ws.numel() * ws.element_size() >= need, lambda: f"ws holds fewer than the {need} bytes this call needs")
     _check_layer(layer, x.device)
     _check_cuda(x, "x")
+    new_out = new_ws = None
     if out is None:
-        out = torch.empty((M, ncols), dtype=x.dtype, device=x.device)
+        out = new_out = x.new_empty((M, ncols))
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        ws = new_ws = x.new_empty(need, dtype=torch.uint8)
     rc = getattr(lib(), fn)(_ptr(x), _dt(x.dtype), _ptr(layer.packed), layer.mode, _ptr(layer.lut),
                             _ptr(layer.perm), *extra, _ptr(out), M, layer.N, layer.K, layer.bits,
                             layer.group_size, _ptr(ws) if need else None, need if need else 0,
                             _stream(stream, x.device))
     _check(fn, rc)
+    _used_on(stream, new_out, new_ws)
     return out
 
 

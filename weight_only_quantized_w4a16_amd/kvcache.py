@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import WQError, _check, _check_cuda, _check_tensor, _dt, _need, _ptr, _stream, lib
+from . import WQError, _check, _check_cuda, _check_tensor, _dt, _need, _ptr, _stream, _used_on, lib
 
 
 @dataclasses.dataclass(frozen=True)
@@ -137,8 +137,9 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
     batch, max_pages = _check_seqs(dev, block_table, kv_lens, cu_q, rows)
     if out is None:
         shape = (rows, cache.kv_heads, cache.head_dim)
-        k, v = data.new_empty(shape, dtype=cache.dtype), data.new_empty(shape, dtype=cache.dtype)
+        k, v = new = data.new_empty(shape, dtype=cache.dtype), data.new_empty(shape, dtype=cache.dtype)
     else:
+        new = ()
         k, v = out
     k_at, ld_k = _check_rows(k, "out[0]", cache, dev, cache.kv_heads, rows)
     v_at, ld_v = _check_rows(v, "out[1]", cache, dev, cache.kv_heads, rows)
@@ -147,6 +148,7 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
                           kv_lens.data_ptr(), _ptr(cu_q), rows, batch, max_pages, cache.num_pages, cache.page_size,
                           cache.kv_heads, cache.head_dim, cache.group, _stream(stream, dev))
     _check("wq_kv_read", rc)
+    _used_on(stream, *new)
     return k, v
 
 
@@ -193,14 +195,16 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     if out is not None:
         o_at, ld_o = _check_rows(out, "out", cache, dev, q_heads, rows)
     _check_cuda(data, "cache.data")
+    new_out = new_ws = None
     if out is None:
-        out = q.new_empty((rows, q_heads, cache.head_dim))
+        out = new_out = q.new_empty((rows, q_heads, cache.head_dim))
         o_at, ld_o = out.data_ptr(), q_heads * cache.head_dim
     if need and ws is None:
-        ws = data.new_empty(need)
+        ws = new_ws = data.new_empty(need)
     rc = L.wq_kv_attention(q_at, ld_q, cache.dt, data.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
                            _ptr(cu_q), o_at, ld_o, rows, batch, max_pages, cache.num_pages, cache.page_size, q_heads,
                            cache.kv_heads, cache.head_dim, cache.group, scale, 1 if causal else 0, window, max_kv_len,
                            ws.data_ptr() if need else None, need, _stream(stream, dev))
     _check("wq_kv_attention", rc)
+    _used_on(stream, new_out, new_ws)
     return out
