@@ -296,9 +296,9 @@ wq_status wq_hadamard(const void* x, wq_dtype dt, void* y, int M, int K, int blo
  * [batch]) is each sequence's length with these rows included: they are its
  * last ones, row i of n at position kv_len - n + i.  block_table (device, int32
  * [batch][max_pages]) names the page of positions page_size p .. + page_size-1.
- * Nothing read from device memory leads outside the buffers: lengths are held
- * to 0 .. max_pages * page_size and row offsets to 0 .. rows; positions whose
- * page number is not in 0 .. num_pages - 1, or that lie below 0, are no place:
+ * Nothing read from device memory leads outside the buffers: row offsets are
+ * held to 0 .. rows, and positions below 0, past the table (max_pages *
+ * page_size) or on a page that is not in 0 .. num_pages - 1 are no place:
  * nothing is written there, they read as zero and attention does not see them.
  * Rows outside every sequence (before cu_q[0], from cu_q[batch] on) are left as
  * they were.
@@ -334,7 +334,7 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  * wq_kv_attention -- out = softmax(scale q K^T) V over the cached values, for
  * prefill, chunks and single tokens alike.
  *   q, out : [rows][q_heads][head_dim] in `dt`, the type of the cache; head h
- *            attends with kv head h / (q_heads / kv_heads)
+ *            attends with kv head h / (q_heads / kv_heads); out may be q itself
  *   scale  : positive and finite
  *   causal : 1: a row sees the positions up to its own; 0: its whole sequence
  *   window : > 0: only the last `window` positions up to its own (0: all)

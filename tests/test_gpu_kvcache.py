@@ -183,6 +183,31 @@ def test_rows_without_a_place(wq):
     torch.cuda.synchronize()
 
 
+def test_lengths_past_the_table(wq):
+    """Rows past the table have no place: they neither move nor touch the cached ones."""
+    P = _kv.Problem([32], None, 1, 64, 64, 16, F16, 61)
+    table = P.table[:, :2].contiguous().cuda()
+    cache = P.empty(wq)
+    wq.wq_kv_write(P.K[0].cuda(), P.V[0].cuda(), cache, table, i32([32]))
+    before = cache.data.clone()
+    x = torch.randn(3, 1, 64).half().cuda()
+    for n in (35, 40, 2 ** 31 - 1):
+        wq.wq_kv_write(x, x, cache, table, i32([n]))
+        assert torch.equal(cache.data, before)
+    # the last of three rows at positions 30, 31, 32
+    wq.wq_kv_write(x, x, cache, table, i32([33]))
+    k, v = wq.wq_kv_read(cache, table, i32([33]), 33)
+    assert same_bits(k[:30], _kv.stored(P.K[0][:30], 64)) and same_bits(k[30:32], _kv.stored(x[:2].cpu(), 64))
+    assert float(k[32].abs().max()) == 0 and float(v[32].abs().max()) == 0
+    # such a row still sees what is there
+    q = torch.randn(1, 2, 64).half()
+    K, V = torch.cat([P.K[0][:30], x[:2].cpu()]), torch.cat([P.V[0][:30], x[:2].cpu()])
+    for n in (33, 50):
+        out = wq.wq_kv_attention(q.cuda(), cache, table, i32([n]), window=40).cpu()
+        want, bound = _kv.attention(q, K, V, torch.tensor([n - 1]), 0.125, True, 40, 64)
+        assert bool(((out.double() - want).abs() <= bound).all())
+
+
 def test_empty_calls(wq):
     cache = wq.wq_kv_cache(1, 16, 1, 64, 64, F16)
     x = torch.empty(0, 1, 64, dtype=F16, device="cuda")
@@ -358,6 +383,20 @@ def test_attention_nan_queries_stay_in_their_rows(wq):
     ok = (out.double() - want).abs() <= bound
     ok[7, 1] = ok[9, 0] = True
     assert bool(ok.all())
+
+
+def test_attention_in_place(wq):
+    """out may be q itself, in every form."""
+    for lens, new, max_kv in (([70], [1], None), ([3000], [1], None), ([300], [80], None), ([90, 200], [1, 9], 100000)):
+        P = _kv.Problem(lens, new, 1, 128, 128, 16, F16, 71)
+        cache = P.empty(wq)
+        P.fill(wq, cache)
+        q = P.queries(4).cuda()
+        args = (cache, P.table.cuda(), i32(lens))
+        cu = P.cu(new).cuda()
+        want = wq.wq_kv_attention(q, *args, cu_q=cu, max_kv_len=max_kv)
+        got = wq.wq_kv_attention(q, *args, cu_q=cu, max_kv_len=max_kv, out=q)
+        assert got.data_ptr() == q.data_ptr() and same_bits(got, want)
 
 
 def test_attention_strided(wq):

@@ -52,20 +52,24 @@ __device__ inline int kv_row_offset(const KvSeqs& s, int b) {
   return v < 0 ? 0 : v > s.rows ? s.rows : v;
 }
 
-// First row, number of rows and length of sequence b.
+// First row, number of rows, position of the first row (below 0 or past the
+// table if the length says so) and length within the table of sequence b.
 struct KvSeq {
-  int row0, n, len;
+  int row0, n, pos0, len;
 };
 __device__ inline KvSeq kv_seq(const KvSeqs& s, int b) {
   KvSeq q;
   q.row0 = kv_row_offset(s, b);
   q.n = kv_row_offset(s, b + 1) - q.row0;
   if (q.n < 0) q.n = 0;
-  const int64_t cap = (int64_t)s.max_pages << (s.rpp_shift + 4);
-  int64_t len = s.lens[b];
+  // (positions of the table are below 2^30 and rows at most 2^24: a length
+  // beyond the first bound has all its rows past the table, and stays in 31 bits)
+  int len = s.lens[b];
   if (len < 0) len = 0;
-  if (len > cap) len = cap;
-  q.len = (int)len;
+  if (len > (1 << 30) + (1 << 25)) len = (1 << 30) + (1 << 25);
+  q.pos0 = len - q.n;
+  const int cap = s.max_pages << (s.rpp_shift + 4);
+  q.len = len < cap ? len : cap;
   return q;
 }
 

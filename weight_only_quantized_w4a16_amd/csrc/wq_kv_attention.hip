@@ -132,7 +132,7 @@ void kv_attention_kernel(const KvAttnArgs a) {
     tile = slot - b * a.tiles;
   }
   const KvSeq sq = kv_seq(a.seqs, b);
-  const int R = a.heads_per_kv, nrows = sq.n * R, pos0 = sq.len - sq.n;
+  const int R = a.heads_per_kv, nrows = sq.n * R, pos0 = sq.pos0;
   const int r0 = tile * BM;  // below 2^31: rows * q_heads <= 2^30
   if (tile < 0 || r0 >= nrows) return;  // the same for every wave of the workgroup
   const int w0 = ROWS ? r0 + wave * 16 * NQ : r0;

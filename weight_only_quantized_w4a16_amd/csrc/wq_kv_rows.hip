@@ -53,16 +53,15 @@ __device__ inline bool kv_item(const KvRowsArgs& a, int lane, KvItem& o) {
     first = b * a.blocks_per_seq;
   }
   const KvSeq q = kv_seq(a.s, b);
-  const int pos0 = q.len - q.n;  // position of the first row, below 0 if the length is too small
-  const int blk = (pos0 >> 4) + (slot - first);
-  o.t0 = pos0 - blk * 16;
+  const int blk = (q.pos0 >> 4) + (slot - first);
+  o.t0 = q.pos0 - blk * 16;
   if (o.t0 < 0) o.t0 = 0;
-  o.t1 = q.len - blk * 16;
+  o.t1 = q.pos0 + q.n - blk * 16;
   if (o.t1 > 16) o.t1 = 16;
   if (o.t0 >= o.t1) return false;
   o.b = b;
   o.blk = blk;
-  o.row0 = (int64_t)q.row0 + (int64_t)blk * 16 - pos0;
+  o.row0 = (int64_t)q.row0 + (int64_t)blk * 16 - q.pos0;
   return true;
 }
 
