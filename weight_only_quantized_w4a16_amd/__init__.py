@@ -92,7 +92,7 @@ def _stream(stream, dev: torch.device) -> int:
     """The stream to launch on: `stream`, or the current stream of `dev`.  The
     library works on the current HIP device (its scratch array is per device),
     so that must be the device of the tensors."""
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
     if dev.index != cur:
         raise ValueError(f"the tensors are on {dev} but the current device is cuda:{cur}; "
                          f"call under torch.cuda.device({dev})")
@@ -250,12 +250,14 @@ def _check_layer(layer: PackedLayer, dev):
     wq_packed_bytes long, the table fp16 [2^bits], the permutation int32 [K],
     all contiguous and on `dev`."""
     p = layer.packed
-    _need(isinstance(p, torch.Tensor) and p.dtype == torch.uint8 and p.dim() == 1 and p.is_contiguous(),
-          "layer.packed must be a contiguous 1-D uint8 tensor")
-    _need(p.device == dev, "x and the layer must be on the same device")
-    _need(p.numel() >= wq_packed_bytes(layer.K, layer.N, layer.bits, layer.group_size, layer.mode),
-          "layer.packed is shorter than the packed size of the layer it describes")
-    _need((layer.lut is not None) == (layer.mode == LUT), "a table is needed exactly in table mode")
+    if not (isinstance(p, torch.Tensor) and p.dtype == torch.uint8 and p.dim() == 1 and p.is_contiguous()):
+        raise ValueError("layer.packed must be a contiguous 1-D uint8 tensor")
+    if p.device != dev:
+        raise ValueError("x and the layer must be on the same device")
+    if p.numel() < lib().wq_packed_bytes(layer.K, layer.N, layer.bits, layer.group_size, layer.mode):
+        raise ValueError("layer.packed is shorter than the packed size of the layer it describes")
+    if (layer.lut is not None) != (layer.mode == LUT):
+        raise ValueError("a table is needed exactly in table mode")
     if layer.lut is not None:
         _check_tensor(layer.lut, "layer.lut", (torch.float16,), (1 << layer.bits,), dev)
     if layer.perm is not None:
@@ -283,9 +285,9 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
     # The kernels take raw pointers: a short or misplaced buffer would be read
     # or written out of bounds on the device, so everything is checked here,
     # before the library is called.
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[1] == layer.K and x.is_contiguous(),
-          "x must be a contiguous [M][K] tensor")
-    _dt(x.dtype)
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[1] == layer.K and x.is_contiguous()):
+        raise ValueError("x must be a contiguous [M][K] tensor")
+    L, dt, dev = lib(), _dt(x.dtype), x.device
     M = x.shape[0]
     fused = "_gate_up" in fn
     if fused != layer.gate_up:
@@ -297,30 +299,32 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
     extra = ()
     if epilogue is not None:
         bias, act, residual = epilogue
-        _need(act in _ACTS, lambda: f"act must be None, 'none', 'relu', 'silu' or 'gelu', got {act!r}")
+        if act not in _ACTS:
+            raise ValueError(f"act must be None, 'none', 'relu', 'silu' or 'gelu', got {act!r}")
         if bias is not None:
-            _check_tensor(bias, "bias", (x.dtype,), (ncols,), x.device)
+            _check_tensor(bias, "bias", (x.dtype,), (ncols,), dev)
         if residual is not None:
-            _check_tensor(residual, "residual", (x.dtype,), (M, ncols), x.device)
+            _check_tensor(residual, "residual", (x.dtype,), (M, ncols), dev)
         extra = (_ptr(bias), _ACTS[act], _ptr(residual))
-    need = wq_workspace_bytes(M, layer.N, layer.K, layer.bits, layer.perm is not None)
+    need = L.wq_workspace_bytes(M, layer.N, layer.K, layer.bits, 0 if layer.perm is None else 1)
     if ws is not None and need:
-        _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == x.device,
+        _need(isinstance(ws, torch.Tensor) and ws.is_contiguous() and ws.device == dev,
               "ws must be a contiguous tensor on the device of x")
         _need(ws.numel() * ws.element_size() >= need, lambda: f"ws holds fewer than the {need} bytes this call needs")
-    _check_layer(layer, x.device)
+    _check_layer(layer, dev)
     _check_cuda(x, "x")
     new_out = new_ws = None
     if out is None:
         out = new_out = x.new_empty((M, ncols))
     if need and ws is None:
         ws = new_ws = x.new_empty(need, dtype=torch.uint8)
-    rc = getattr(lib(), fn)(_ptr(x), _dt(x.dtype), _ptr(layer.packed), layer.mode, _ptr(layer.lut),
-                            _ptr(layer.perm), *extra, _ptr(out), M, layer.N, layer.K, layer.bits,
-                            layer.group_size, _ptr(ws) if need else None, need if need else 0,
-                            _stream(stream, x.device))
-    _check(fn, rc)
-    _used_on(stream, new_out, new_ws)
+    rc = getattr(L, fn)(x.data_ptr(), dt, layer.packed.data_ptr(), layer.mode, _ptr(layer.lut), _ptr(layer.perm),
+                        *extra, out.data_ptr(), M, layer.N, layer.K, layer.bits, layer.group_size,
+                        ws.data_ptr() if need else None, need, _stream(stream, dev))
+    if rc:
+        raise WQError(fn, rc)
+    if stream is not None:
+        _used_on(stream, new_out, new_ws)
     return out
 
 

@@ -29,8 +29,23 @@
 // shows times v / s rather than times c: lo / s, as the sum of two fp16, is one
 // more operand tile of the second product (rows 0 and 1 of it).  fp16 outputs,
 // one row over 1037 keys: 0.39e-3 of the norm when the offsets were summed apart,
-// LATER now; the rounding of the output alone is 0.20e-3.  A group without a step
+// 0.22e-3 now; the rounding of the output alone is 0.20e-3.  A group without a step
 // (all channels alike) takes |lo| for one.  Scores, maxima and sums are fp32.
+//
+// What bounds it (D = 128, one group, MI355X).  Decode: the bytes of the cache --
+// 48 rows of 8 heads over 2000 to 8000 keys, 260 MB, in 54-57 us, 4.6-4.8 TB/s
+// where a copy of 4 GiB reaches 4.9; about half of the vector instructions' time
+// fits beside it.  Many rows: vector instructions.  For a block of 64 keys and 32
+// rows a wave issues 500 of them (160 unpack 32 words of codes, which two row
+// tiles share; about nine for each of a lane's 32 scores, one of them the
+// exponential at a quarter of the rate) beside 68 MFMAs of 16 cycles: 4096-row
+// prompts run in 345 us (797 TFLOP/s, vector units 82 % busy, matrix units 33 %).
+// Measured and not kept: three and four row tiles per wave (their sums spill or
+// leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
+// against 140 on 1792 rows of 7 sequences), runs of blocks with and without hidden
+// keys in loops of their own (copies of the sums, spills: 2066 us), wave
+// priorities (-3 to +7 % by shape), the offsets' start of the scores from the
+// matrix cores (351 us).
 //
 // Two forms.  Few rows per sequence (decode): the waves of a workgroup
 // take the blocks of 64 keys in turn and merge through LDS.  Many rows: each
@@ -607,8 +622,9 @@ void kv_attention_kernel(const KvAttnArgs a) {
 
 // Joins the parts of the keys: one workgroup per (row, head), as many parts at
 // a time as it has rows of D / 4 threads, the parts of a thread and then the
-// threads of a channel in order.  (64 parts of 64 rows, D = 128: 50 us with one
-// wave that took the parts one after the other, LATER.)
+// threads of a channel in order: a fixed order, so the same call gives the same
+// bits.  Latency bound: 64 parts of 64 rows, D = 128, in 4.2 us (50 us with one
+// wave that took the parts one after the other).
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttnArgs a) {
   constexpr int VL = D / 4;

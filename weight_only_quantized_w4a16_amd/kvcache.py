@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import WQError, _check, _check_cuda, _check_tensor, _dt, _need, _ptr, _stream, _used_on, lib
+from . import WQError, _check_cuda, _check_tensor, _dt, _need, _ptr, _stream, _used_on, lib
 
 
 @dataclasses.dataclass(frozen=True)
@@ -97,8 +97,11 @@ def _check_seqs(dev, block_table, kv_lens, cu_q, rows: int) -> Tuple[int, int]:
     if not (isinstance(block_table, torch.Tensor) and block_table.dim() == 2):
         raise ValueError("block_table must be a [batch][pages] tensor")
     batch, max_pages = block_table.shape
-    _check_tensor(block_table, "block_table", (torch.int32,), (batch, max_pages), dev)
-    _check_tensor(kv_lens, "kv_lens", (torch.int32,), (batch,), dev)
+    if not (block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.device == dev
+            and isinstance(kv_lens, torch.Tensor) and kv_lens.dtype == torch.int32 and kv_lens.shape == (batch,)
+            and kv_lens.is_contiguous() and kv_lens.device == dev):
+        _check_tensor(block_table, "block_table", (torch.int32,), (batch, max_pages), dev)
+        _check_tensor(kv_lens, "kv_lens", (torch.int32,), (batch,), dev)
     if cu_q is not None:
         _check_tensor(cu_q, "cu_q", (torch.int32,), (batch + 1,), dev)
     elif rows and (batch == 0 or rows % batch):
@@ -122,7 +125,8 @@ def wq_kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: t
     rc = lib().wq_kv_write(k_at, v_at, ld_k, ld_v, cache.dt, data.data_ptr(), block_table.data_ptr(),
                            kv_lens.data_ptr(), _ptr(cu_q), rows, batch, max_pages, cache.num_pages, cache.page_size,
                            cache.kv_heads, cache.head_dim, cache.group, _stream(stream, dev))
-    _check("wq_kv_write", rc)
+    if rc:
+        raise WQError("wq_kv_write", rc)
 
 
 def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor, rows: int,
@@ -136,8 +140,9 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
         raise ValueError("rows must be a count")
     batch, max_pages = _check_seqs(dev, block_table, kv_lens, cu_q, rows)
     if out is None:
-        shape = (rows, cache.kv_heads, cache.head_dim)
-        k, v = new = data.new_empty(shape, dtype=cache.dtype), data.new_empty(shape, dtype=cache.dtype)
+        k = torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=cache.dtype, device=dev)
+        v = torch.empty_like(k)
+        new = (k, v)
     else:
         new = ()
         k, v = out
@@ -147,8 +152,10 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
     rc = lib().wq_kv_read(data.data_ptr(), k_at, v_at, ld_k, ld_v, cache.dt, block_table.data_ptr(),
                           kv_lens.data_ptr(), _ptr(cu_q), rows, batch, max_pages, cache.num_pages, cache.page_size,
                           cache.kv_heads, cache.head_dim, cache.group, _stream(stream, dev))
-    _check("wq_kv_read", rc)
-    _used_on(stream, *new)
+    if rc:
+        raise WQError("wq_kv_read", rc)
+    if stream is not None:
+        _used_on(stream, *new)
     return k, v
 
 
@@ -197,7 +204,7 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _check_cuda(data, "cache.data")
     new_out = new_ws = None
     if out is None:
-        out = new_out = q.new_empty((rows, q_heads, cache.head_dim))
+        out = new_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         o_at, ld_o = out.data_ptr(), q_heads * cache.head_dim
     if need and ws is None:
         ws = new_ws = data.new_empty(need)
@@ -205,6 +212,8 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                            _ptr(cu_q), o_at, ld_o, rows, batch, max_pages, cache.num_pages, cache.page_size, q_heads,
                            cache.kv_heads, cache.head_dim, cache.group, scale, 1 if causal else 0, window, max_kv_len,
                            ws.data_ptr() if need else None, need, _stream(stream, dev))
-    _check("wq_kv_attention", rc)
-    _used_on(stream, new_out, new_ws)
+    if rc:
+        raise WQError("wq_kv_attention", rc)
+    if stream is not None:
+        _used_on(stream, new_out, new_ws)
     return out
