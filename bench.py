@@ -53,6 +53,7 @@ METRIC = "weight GB/s (GEMV, M=1) & TFLOP/s (GEMM, M=2048) as % of HBM/MFMA roof
 KERNEL_SOURCES = ["wq_gemv.hip", "wq_decode.hpp", "wq_layout.hpp"]  # the dominant (GEMV) kernel's sources
 ALL_SOURCES = ["wq_api.hip", "wq_common.hpp", "wq_decode.hpp", "wq_gemm.hip", "wq_gemv.hip", "wq_hadamard.hip",
                "wq_layout.hpp"]
+KV_SOURCES = ["wq_kv.hpp", "wq_kv_api.hip", "wq_kv_attention.hip", "wq_kv_rows.hip"]
 
 
 def parse():
@@ -87,6 +88,11 @@ def parse():
                         "cid/layer/bits/group/M (e.g. 5/wide/4/32/1), for rocprofv3 runs; 'copy' "
                         "adds a 256 MiB device copy (counter calibration)")
     p.add_argument("--profile-reps", type=int, default=40)
+    p.add_argument("--operators", nargs="*", default=None, metavar="CASE",
+                   help="instead of the step: time the cases of perf/operators.py (the 4-bit cache, attention over it, "
+                        "epilogue products; all of them when none is named), graph-replayed")
+    p.add_argument("--profile-operator", default="", metavar="CASE",
+                   help="instead of the step: one case of perf/operators.py, warmed and run --profile-reps times")
     return p.parse_args()
 
 
@@ -310,6 +316,63 @@ def run_profile_cases(args):
         torch.cuda.empty_cache()
 
 
+def operator_cases():
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    return ops
+
+
+def run_operators(args):
+    """The measured cases of the cache operators and the epilogue product through the package, one JSON line each:
+    three states in turn, ten rounds captured in a HIP graph, median of 5 replays after the warm-up.  Bytes and FLOP
+    are what the operator cannot do without."""
+    import torch
+    torch.cuda.set_device(0)
+    stream = torch.cuda.current_stream()
+    ops = operator_cases()
+    for case in ops.listed():
+        if args.operators and case["name"] not in args.operators:
+            continue
+        states = [ops.prepare(case, seed) for seed in range(3)]
+        for st in states:
+            ops.run(st)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(30):
+                ops.run(states[i % 3])
+        warm_up(stream, graph.replay)
+        times = []
+        for _ in range(5):
+            e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            e0.record(stream)
+            graph.replay()
+            e1.record(stream)
+            torch.cuda.synchronize()
+            times.append(e0.elapsed_time(e1) / 30 * 1e3)
+        us, w = sorted(times)[2], ops.work(case)
+        print(json.dumps({"case": case["name"], "us": round(us, 2), "GBps": round(w["bytes"] / us / 1e3, 1),
+                          "TFLOPs": round(w["flops"] / us / 1e6, 2)}), flush=True)
+        del states, graph
+        torch.cuda.empty_cache()
+
+
+def run_profile_operator(args):
+    import torch
+    torch.cuda.set_device(0)
+    ops = operator_cases()
+    case = next(c for c in ops.listed() if c["name"] == args.profile_operator)
+    st = ops.prepare(case, 0)
+    warm_up(torch.cuda.current_stream(), lambda: [ops.run(st) for _ in range(10)])
+    for _ in range(args.profile_reps):
+        ops.run(st)
+    torch.cuda.synchronize()
+    print(json.dumps({"case": case["name"], "calls": args.profile_reps}), flush=True)
+
+
 def _match(spec, cid, lname, bits, M):
     f = spec.split("/") + ["*"] * 4
     return ((f[0] in ("*", str(cid))) and (f[1] in ("*", lname)) and (f[2] in ("*", str(bits)))
@@ -451,6 +514,12 @@ def main():
         return
     if args.profile_case:
         run_profile_cases(args)
+        return
+    if args.operators is not None:
+        run_operators(args)
+        return
+    if args.profile_operator:
+        run_profile_operator(args)
         return
 
     import numpy as np
