@@ -148,8 +148,7 @@ struct KvPlan {
 // the sums of a tile take 16 registers per lane for every 64 channels, the
 // offsets 4 for every group, and 256 registers are to hold it all.
 constexpr bool kv_two_tiles(int head_dim, int group) { return head_dim <= 128 && head_dim / group <= 2; }
-// Waves per SIMD the registers of the one-tile key form leave room for, that is
-// workgroups of four waves per CU.
+// Waves per SIMD the registers of the one-tile key form leave room for.
 constexpr int kv_key_waves(int head_dim, int group) {
   return head_dim == 64 || (head_dim == 128 && group == 128) ? 3 : 2;
 }
@@ -164,16 +163,28 @@ inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv
   const int bm = (p.rows_form ? 64 : 16) * p.nq;
   p.tiles = (int)((per + bm - 1) / bm);
   p.slots = ragged ? (int)((int64_t)rows * heads_per_kv / bm + batch) : p.tiles * batch;
-  // Parts: as many as leave all workgroups resident at once (a few more would
-  // wait for a second round: one row of 64 heads over 131071 keys, group 64, two
-  // to a CU: 33 us with 512 workgroups, 38 with 768; 48 rows over up to 8000,
-  // three to a CU: 57.8 us with 384, 53.9 with 768, 57.6 with 1920), each of at
-  // least one round of blocks of 64 keys for the key form (a row over 1037 keys,
-  // 32 heads: 10.0 us in 5 parts, 11.7 in 2), four blocks for the row form.
+  // Parts.  Row form: about two workgroups to a CU (its limit by registers).
+  // Key form: 256 workgroups of four waves already take the memory's rate, so
+  // the parts only even out what each CU gets: the part count of least
+  // ceil(workgroups / 256) / parts, with 4 % for every workgroup of a CU.
+  // (131071 keys of 8 heads: 34.9 us with 256 workgroups, 35.7 with 512, 39.1 with
+  // 768; 192 workgroups over up to 16000 keys: 84 us whole, 60 in 4 parts; 256
+  // over up to 4000: 26.7 us whole, 28.8 in 2.)  A part has at least one round
+  // of blocks of 64 keys in the key form (a row over 1037 keys, 32 heads: 10.0 us
+  // in 5 parts, 11.7 in 2), four blocks in the row form.
   const int64_t wgs = (int64_t)p.slots * kv_heads;
-  const int64_t room = 256 * (p.nq == 1 && !p.rows_form ? kv_key_waves(head_dim, group) : 2);
   const int64_t rounds = p.rows_form ? max_kv / 256 : (max_kv + 255) / 256;
-  int64_t s = wgs >= room ? 1 : room / wgs;
+  int64_t s = p.rows_form ? (wgs >= 512 ? 1 : 512 / wgs) : 1;
+  if (!p.rows_form) {
+    double best = 1e30;
+    for (int64_t t = 1; t <= kKvMaxSplits && t <= rounds && (t == 1 || t * wgs <= 1024); ++t) {
+      const double cost = (double)((t * wgs + 255) / 256) / (double)t * (1.0 + 0.04 * (double)(t * wgs) / 256.0);
+      if (cost < best) {
+        best = cost;
+        s = t;
+      }
+    }
+  }
   if (s > rounds) s = rounds;
   if (s > kKvMaxSplits) s = kKvMaxSplits;
   p.splits = s < 1 ? 1 : (int)s;
