@@ -340,7 +340,10 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  *   window : > 0: only the last `window` positions up to its own (0: all)
  *   max_kv_len : the longest kv_len to expect; it shapes the launch only (the
  *            result is right for any lengths)
- *   ws     : wq_kv_workspace_bytes() bytes, 16-byte aligned (may be NULL when 0)
+ *   ws     : wq_kv_workspace_bytes() bytes for these sizes (ragged: cu_q given),
+ *            16-byte aligned (may be NULL when 0).  Fewer rows may need more, as
+ *            their keys are split further.  Calls that overlap in time must not
+ *            share it; nothing in it needs to start at any value
  * A row that sees no position is zero.  Scores, softmax and sums are fp32; the
  * product of a probability and a value step is rounded to fp16 once, and the
  * output to `dt` once.  Value steps s are expected in 2^-60 .. 2^100 (smaller

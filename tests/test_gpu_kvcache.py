@@ -269,6 +269,19 @@ def test_attention_masks(wq, new, causal, window):
     check_attention(wq, _kv.Problem([200, 260], [new, new], 1, 64, 32, 16, BF16, new), 2, causal, window)
 
 
+def test_attention_sizes_past_32_bits(wq):
+    """A window or an expected length that no 32-bit count holds means all there is."""
+    P = _kv.Problem([100], [3], 1, 64, 64, 16, F16, 8)
+    cache = P.empty(wq)
+    P.fill(wq, cache)
+    q = P.queries(2).cuda()
+    args = (q, cache, P.table.cuda(), i32([100]))
+    want = wq.wq_kv_attention(*args)
+    for n in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 40):
+        assert same_bits(wq.wq_kv_attention(*args, window=n), want)
+        assert same_bits(wq.wq_kv_attention(*args, max_kv_len=n), want)
+
+
 @pytest.mark.parametrize("D,G,dt", [(128, 128, F16), (128, 64, BF16), (64, 32, F16), (256, 64, BF16)])
 def test_attention_long_context_in_parts(wq, D, G, dt):
     """Few rows over many keys: the keys are split over workgroups and joined."""
@@ -279,6 +292,27 @@ def test_attention_long_context_in_parts(wq, D, G, dt):
     P = _kv.Problem([2100, 64], [40, 64], 1, D, G, 64, dt, D)
     assert wq.wq_kv_workspace_bytes(104, 2, True, 4, 1, D, G, 2100) > 0
     check_attention(wq, P, 4)
+
+
+@pytest.mark.parametrize("D,G,dt", [(128, 64, F16), (96, 32, BF16), (256, 128, F16)])
+def test_attention_many_rows_in_few_parts(wq, D, G, dt):
+    """Thousands of (row, head) outputs joined from a few parts, among them rows that some parts hold no key for and
+    rows of no sequence."""
+    P = _kv.Problem([1900, 550], [300, 250], 1, D, G, 32, dt, D + 1)
+    per = wq.wq_kv_workspace_bytes(560, 2, True, 4, 1, D, G, 1900) // (560 * 4 * (D + 2) * 4)
+    assert 2 <= per <= 8
+    cache = P.empty(wq)
+    P.fill(wq, cache)
+    q = P.queries(4)
+    wide = torch.zeros(560, 4, D, dtype=dt)
+    wide[5:555] = q
+    out = torch.full((560, 4, D), 2.0, dtype=dt, device="cuda")
+    wq.wq_kv_attention(wide.cuda(), cache, P.table.cuda(), i32(P.lens), cu_q=i32([5, 305, 555]), window=700,
+                       max_kv_len=1900, out=out)
+    want, bound = P.reference(q, D ** -0.5, True, 700)
+    got = out.cpu().double()
+    assert bool(((got[5:555] - want).abs() <= bound).all())
+    assert bool((got[:5] == 2).all()) and bool((got[555:] == 2).all())
 
 
 @pytest.mark.parametrize("max_kv", [0, 1, 64, 5000, 10 ** 8])

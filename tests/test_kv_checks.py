@@ -159,6 +159,8 @@ def test_binding_refuses(cache):
         wq.wq_kv_attention(x, cache, t, l, out=rows_of(3))
     with pytest.raises(ValueError, match="ws holds fewer"):
         wq.wq_kv_attention(x, cache, t, l, max_kv_len=100000, ws=torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="num_pages"):
+        wq.KVCache(cache.data, (1 << 32) + 4, 16, 2, 64, 64, torch.float16)
     short = wq.KVCache(cache.data[:-1], 4, 16, 2, 64, 64, torch.float16)
     with pytest.raises(ValueError, match="shorter"):
         wq.wq_kv_write(x, x, short, t, l)

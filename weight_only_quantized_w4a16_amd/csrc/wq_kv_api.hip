@@ -139,7 +139,8 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
   KvPlan p;
   if (!plan_of(p, rows, batch, cu_q != nullptr, q_heads, kv_heads, head_dim, group, max_kv_len))
     return WQ_EUNSUPPORTED;
-  if ((int64_t)p.slots * p.splits * kv_heads >= ((int64_t)1 << 31) || (int64_t)rows * q_heads > ((int64_t)1 << 30))
+  // one grid dimension: workgroups of up to 512 threads, fewer than 2^32 threads
+  if ((int64_t)p.slots * p.splits * kv_heads >= ((int64_t)1 << 23) || (int64_t)rows * q_heads > ((int64_t)1 << 30))
     return WQ_EUNSUPPORTED;
   const size_t part = kv_part_bytes(p, rows, q_heads, head_dim), need = part + kv_ml_bytes(p, rows, q_heads);
   if (need && (!ws || ws_bytes < need)) return WQ_ENOSPACE;
@@ -153,7 +154,7 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
   a.heads_per_kv = q_heads / kv_heads;
   a.scale_log2 = scale * 1.44269504088896340736f;
   a.causal = causal;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // positions are below that
   a.splits = p.splits;
   a.part = need ? (float*)ws : nullptr;
   a.part_ml = need ? (float*)((uint8_t*)ws + part) : nullptr;
