@@ -279,7 +279,9 @@ def test_attention_sizes_past_32_bits(wq):
     want = wq.wq_kv_attention(*args)
     for n in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 40):
         assert same_bits(wq.wq_kv_attention(*args, window=n), want)
-        assert same_bits(wq.wq_kv_attention(*args, max_kv_len=n), want)
+        got = wq.wq_kv_attention(*args, max_kv_len=n).cpu().double()
+        ref, bound = P.reference(q.cpu(), 0.125)
+        assert bool(((got - ref).abs() <= bound).all())
 
 
 @pytest.mark.parametrize("D,G,dt", [(128, 128, F16), (128, 64, BF16), (64, 32, F16), (256, 64, BF16)])

@@ -164,8 +164,8 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
 
 def wq_kv_workspace_bytes(rows: int, batch: int, ragged: bool, q_heads: int, kv_heads: int, head_dim: int,
                           group: int, max_kv_len: int) -> int:
-    """Scratch of a wq_kv_attention call with these sizes (ragged: with cu_q; max_kv_len: at most the table's
-    capacity).  Fewer rows may need more of it: ask for every shape that is used."""
+    """Scratch of a wq_kv_attention call with these sizes (ragged: with cu_q; max_kv_len: at most 2^30).
+    Fewer rows may need more of it: ask for every shape that is used."""
     return int(lib().wq_kv_workspace_bytes(rows, batch, int(bool(ragged)), q_heads, kv_heads, head_dim, group,
                                            max_kv_len))
 
@@ -195,13 +195,12 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
         raise ValueError(f"window must be 0 or a count, got {window}")
     if window > 1 << 30:  # no position lies that far back
         window = 1 << 30
-    room = max_pages * cache.page_size
     if max_kv_len is None:
-        max_kv_len = room
+        max_kv_len = max_pages * cache.page_size
     elif not (isinstance(max_kv_len, int) and max_kv_len >= 0):
         raise ValueError("max_kv_len must be a count")
-    elif max_kv_len > room:
-        max_kv_len = room
+    if max_kv_len > 1 << 30:
+        max_kv_len = 1 << 30
     L = lib()
     need = L.wq_kv_workspace_bytes(rows, batch, cu_q is not None, q_heads, cache.kv_heads, cache.head_dim,
                                    cache.group, max_kv_len)
