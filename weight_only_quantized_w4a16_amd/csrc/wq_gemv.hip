@@ -547,36 +547,45 @@ __global__ __launch_bounds__((gemv_big_frames<BITS, TN, GPU, MR>() ? 512 : 1024)
   __syncthreads();
   static_assert(!SWIGLU || TN == 1, "gate and up tiles sit on different waves");
   constexpr int SLOTS = TN * MR * NRED * 64;
-  for (int i = threadIdx.x; i < SLOTS; i += a.waves * 64) {
-    const int l = i & 63, e = (i >> 6) % NRED, rb = (i / (64 * NRED)) % MR, t = i / (64 * NRED * MR);
-    // sum over the waves w0, w0 + step, ... of tile t's partial results
-    auto reduce = [&](int w0, int step) {
-      float v = 0.0f;
-      for (int w = w0; w < a.waves; w += step) v += red[(size_t)w * WSTRIDE + ((t * MR + rb) * NRED + e) * 64 + l];
-      return v;
-    };
-    float v;
-    if constexpr (SWIGLU) {
-      const float g = reduce(0, 2), u = reduce(1, 2);
-      v = g / (1.0f + expf(-g)) * u;
-    } else {
-      v = reduce(0, 1);
-    }
-    // packed: lane l = 16 m + col; packed 8: row 2 (l / 16) + e, col l % 16;
-    // standard: row 16 rb + 4 (l / 16) + e, col l % 16
-    const int m = PK == 4 ? (l >> 4) : PK == 8 ? 2 * (l >> 4) + e : 16 * rb + 4 * (l >> 4) + e;
-    const int n = (SWIGLU ? (int)blockIdx.x : nt0 + t) * 16 + (l & 15);
-    if (m < a.M) {
-      if constexpr (!SWIGLU) {
-        if (a.epi.on) {
+  // the epilogue product's loop is one of its own, so that the plain product's
+  // tail carries nothing of it
+  auto finish = [&](auto epilogue) __attribute__((always_inline)) {
+    for (int i = threadIdx.x; i < SLOTS; i += a.waves * 64) {
+      const int l = i & 63, e = (i >> 6) % NRED, rb = (i / (64 * NRED)) % MR, t = i / (64 * NRED * MR);
+      // sum over the waves w0, w0 + step, ... of tile t's partial results
+      auto reduce = [&](int w0, int step) {
+        float v = 0.0f;
+        for (int w = w0; w < a.waves; w += step) v += red[(size_t)w * WSTRIDE + ((t * MR + rb) * NRED + e) * 64 + l];
+        return v;
+      };
+      float v;
+      if constexpr (SWIGLU) {
+        const float g = reduce(0, 2), u = reduce(1, 2);
+        v = g / (1.0f + expf(-g)) * u;
+      } else {
+        v = reduce(0, 1);
+      }
+      // packed: lane l = 16 m + col; packed 8: row 2 (l / 16) + e, col l % 16;
+      // standard: row 16 rb + 4 (l / 16) + e, col l % 16
+      const int m = PK == 4 ? (l >> 4) : PK == 8 ? 2 * (l >> 4) + e : 16 * rb + 4 * (l >> 4) + e;
+      const int n = (SWIGLU ? (int)blockIdx.x : nt0 + t) * 16 + (l & 15);
+      if (m < a.M) {
+        if constexpr (decltype(epilogue)::value) {
           if (a.epi.bias) v += elem_to_f32<DT>(a.epi.bias[n]);
           v = smooth_act(a.epi.act) ? activate<true>(v, a.epi.act) : activate<false>(v, a.epi.act);
           if (a.epi.residual) v += elem_to_f32<DT>(a.epi.residual[(size_t)m * a.ldy + n]);
         }
+        a.y[(size_t)m * a.ldy + n] = DT == F16 ? f32_to_f16(v) : f32_to_bf16(v);
       }
-      a.y[(size_t)m * a.ldy + n] = DT == F16 ? f32_to_f16(v) : f32_to_bf16(v);
+    }
+  };
+  if constexpr (!SWIGLU) {
+    if (a.epi.on) {
+      finish(std::true_type{});
+      return;
     }
   }
+  finish(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
