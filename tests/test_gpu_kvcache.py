@@ -449,6 +449,28 @@ def test_attention_strided(wq):
     assert bool((o[:, :128] == 9).all()) and bool((o[:, 5 * 128:] == 9).all())
 
 
+def test_attention_of_rotated_rows(wq):
+    """Queries and keys rotated head by head (wq_hadamard) before they are cached: the same attention, with an outlier
+    channel spread over its group."""
+    H, D, n = 2, 128, 150
+    P = _kv.Problem([n], [5], H, D, 128, 16, F16, 91)
+    P.K[0][:, :, 17] *= 12
+    q = P.queries(4)
+    a = torch.softmax(q[:, 0].double() @ P.K[0][:, 0].double().T * 0.05 + torch.full((5, n), 0.0).masked_fill(
+        torch.arange(n)[None] > torch.arange(n - 5, n)[:, None], -math.inf).double(), 1) @ P.V[0][:, 0].double()
+    rot = lambda x: wq.wq_hadamard(x.reshape(-1, D).cuda(), D).view(x.shape)
+    errors = []
+    for turn in (lambda x: x.cuda(), rot):
+        kq, kk = turn(q), turn(P.K[0])
+        cache = wq.wq_kv_cache(P.num_pages, 16, H, D, 128, F16)
+        wq.wq_kv_write(kk, P.V[0].cuda(), cache, P.table.cuda(), i32([n]))
+        out = wq.wq_kv_attention(kq, cache, P.table.cuda(), i32([n]), scale=0.05).cpu()
+        want, bound = _kv.attention(kq.cpu(), kk.cpu(), P.V[0], torch.arange(n - 5, n), 0.05, True, 0, 128)
+        assert bool(((out.double() - want).abs() <= bound).all())
+        errors.append(float((out[:, 0].double() - a).norm() / a.norm()))
+    assert errors[1] < errors[0]  # the rotated keys lose less to 4 bits
+
+
 def test_cache_beyond_4_gib(wq):
     """Pages whose bytes lie past 32-bit offsets."""
     H, D, page = 8, 128, 1024
