@@ -36,10 +36,10 @@
 // 48 rows of 8 heads over 2000 to 8000 keys, 260 MB, in 54-57 us, 4.6-4.8 TB/s
 // where a copy of 4 GiB reaches 4.9; about half of the vector instructions' time
 // fits beside it.  Many rows: vector instructions.  For a block of 64 keys and 32
-// rows a wave issues 500 of them (160 unpack 32 words of codes, which two row
-// tiles share; about nine for each of a lane's 32 scores, one of them the
+// rows a wave issues about 500 of them (160 unpack 32 words of codes, which two
+// row tiles share; about nine for each of a lane's 32 scores, one of them the
 // exponential at a quarter of the rate) beside 68 MFMAs of 16 cycles: 4096-row
-// prompts run in 345 us (797 TFLOP/s, vector units 82 % busy, matrix units 33 %).
+// prompts run in 345 us (797 TFLOP/s, vector units 83 % busy, matrix units 33 %).
 // Measured and not kept: three and four row tiles per wave (their sums spill or
 // leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
 // against 140 on 1792 rows of 7 sequences), runs of blocks with and without hidden
@@ -82,6 +82,15 @@ __device__ inline uint32_t row_bcast_u(uint32_t v) {
 template <int I>
 __device__ inline float row_bcast(float v) {
   return __uint_as_float(row_bcast_u<I>(__float_as_uint(v)));
+}
+
+// Largest of three; a NaN among them may or may not show.  The instruction
+// itself: the library's maximum quiets every operand with one of its own first,
+// 32 more for a block of 64 keys and 32 rows.
+__device__ inline float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
 }
 
 // W consecutive words, W = 2, 3, 4, 6 or 8
@@ -323,9 +332,10 @@ void kv_attention_kernel(const KvAttnArgs a) {
       f4 d[NQ][4];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        // a copy for every tile: the broadcasts then stay operand modifiers
+        // a copy for every tile: the broadcasts then stay operand modifiers (not
+        // where it would spill: D = 128 in two groups, 502 us against 475)
         float r = kr[g];
-        if (NQ > 1) asm volatile("" : "+v"(r));
+        if (NQ > 1 && (NG == 1 || D == 64)) asm volatile("" : "+v"(r));
         sfor<16>([&](auto ic) __attribute__((always_inline)) {
           constexpr int i = decltype(ic)::value;
           d[n][i / 4][i % 4] = row_bcast<i>(r) * qs[n][g];
@@ -346,14 +356,16 @@ void kv_attention_kernel(const KvAttnArgs a) {
           for (int n = 0; n < NQ; ++n) d[n][j] = mfma16<F16>(kf, q[n], d[n][j]);
         }
       }
-      sfor<16>([&](auto ic) __attribute__((always_inline)) {
-        constexpr int i = decltype(ic)::value;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          const float x = row_bcast<i>(ks[g]) * d[n][i / 4][i % 4];
+      for (int n = 0; n < NQ; ++n) {
+        float s = ks[g];
+        if (NQ > 1 && (NG == 1 || D == 64)) asm volatile("" : "+v"(s));
+        sfor<16>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          const float x = row_bcast<i>(s) * d[n][i / 4][i % 4];
           u[n][i / 4][i % 4] = g == 0 ? x : u[n][i / 4][i % 4] + x;
-        }
-      });
+        });
+      }
     }
     scored();
     // step and offset / step of this lane's value
@@ -393,10 +405,10 @@ void kv_attention_kernel(const KvAttnArgs a) {
           for (int i = 0; i < 4; ++i)
             if (4 * j + i >= a1 || 4 * j + i < a0) u[n][j][i] = -INFINITY;
       }
-      float t = fmaxf(fmaxf(u[n][0][0], u[n][0][1]), fmaxf(u[n][0][2], u[n][0][3]));
+      float t = max3(u[n][0][0], u[n][0][1], u[n][0][2]);
 #pragma unroll
-      for (int j = 1; j < 4; ++j)
-        t = fmaxf(t, fmaxf(fmaxf(u[n][j][0], u[n][j][1]), fmaxf(u[n][j][2], u[n][j][3])));
+      for (int i = 3; i < 15; i += 2) t = max3(t, u[n][i / 4][i % 4], u[n][(i + 1) / 4][(i + 1) % 4]);
+      t = max3(t, u[n][3][3], t);
       top[n] = t * cq[n];
       over |= top[n] > m[n] + kSlack;
     }
