@@ -36,13 +36,13 @@
 // 48 rows of 8 heads over 2000 to 8000 keys, 260 MB, in 54-57 us, 4.6-4.8 TB/s
 // where a copy of 4 GiB reaches 4.9; about half of the vector instructions' time
 // fits beside it.  Many rows: vector instructions.  For a block of 64 keys and 32
-// rows a wave issues about 500 of them (160 unpack 32 words of codes, which two
+// rows a wave issues about 490 of them (160 unpack 32 words of codes, which two
 // row tiles share; about nine for each of a lane's 32 scores, one of them the
 // exponential at a quarter of the rate) beside 68 MFMAs of 16 cycles: 4096-row
-// prompts run in 345 us (797 TFLOP/s, vector units 83 % busy, matrix units 33 %).
+// prompts run in 344 us (799 TFLOP/s, vector units 83 % busy, matrix units 33 %).
 // Measured and not kept: three and four row tiles per wave (their sums spill or
 // leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
-// against 140 on 1792 rows of 7 sequences), runs of blocks with and without hidden
+// against 137 on 1792 rows of 7 sequences), runs of blocks with and without hidden
 // keys in loops of their own (copies of the sums, spills: 2066 us), wave
 // priorities (-3 to +7 % by shape), the offsets' start of the scores from the
 // matrix cores (351 us).
@@ -84,13 +84,12 @@ __device__ inline float row_bcast(float v) {
   return __uint_as_float(row_bcast_u<I>(__float_as_uint(v)));
 }
 
-// Largest of three; a NaN among them may or may not show.  The instruction
-// itself: the library's maximum quiets every operand with one of its own first,
-// 32 more for a block of 64 keys and 32 rows.
+// Largest of three, NaN if one of them is: one instruction.  (The maximum that
+// drops NaN quiets every operand with one of its own first, 32 more for a block
+// of 64 keys and 32 rows; written as inline assembly it would be outside the
+// compiler's view of what the matrix cores still read.)
 __device__ inline float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // W consecutive words, W = 2, 3, 4, 6 or 8
