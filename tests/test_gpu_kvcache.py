@@ -421,6 +421,27 @@ def test_attention_nan_queries_stay_in_their_rows(wq):
     assert bool(ok.all())
 
 
+@pytest.mark.parametrize("dt", [F16, torch.bfloat16])
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([20], [3]), ([70], [40])])
+def test_attention_infinite_queries_are_nan(wq, dt, lens, new):
+    """An infinite channel of a query whose keys all have the same sign there: every score is the same infinity, and
+    the softmax of that is NaN; a row of the same call without a position stays zero."""
+    P = _kv.Problem(lens, new, 1, 64, 64, 16, dt, 77)
+    P.K[0].abs_().add_(1)
+    cache = P.empty(wq)
+    P.fill(wq, cache)
+    for sign in (math.inf, -math.inf):
+        q = P.queries(2)
+        q[:, 0, 5] = sign
+        q[-1, 0] = P.queries(2)[-1, 0]
+        q[-1, 1, 63] = sign
+        out = wq.wq_kv_attention(q.cuda(), cache, P.table.cuda(), i32(lens)).cpu()
+        bad = q.isinf().any(-1)
+        assert bool(out[bad].isnan().all()) and bool(out[~bad].isfinite().all())
+        none = wq.wq_kv_attention(q.cuda(), cache, P.table.cuda(), i32([0])).cpu()
+        assert bool((none == 0).all())
+
+
 def test_attention_in_place(wq):
     """out may be q itself, in every form."""
     for lens, new, max_kv in (([70], [1], None), ([3000], [1], None), ([300], [80], None), ([90, 200], [1, 9], 100000)):

@@ -200,9 +200,12 @@ void kv_attention_kernel(const KvAttnArgs a) {
     big = fmaxf(big, __shfl_xor(big, 16, 64));
     big = fmaxf(big, __shfl_xor(big, 32, 64));
     int ex = (int)((__float_as_uint(big) >> 23) & 255) - 127;  // floor(log2 big)
-    if (ex == 128) ex = 13;                                     // an infinity: the row is NaN anyway
+    // an infinite channel makes every score infinite or NaN and the row NaN; as
+    // infinities, scores that are all -inf would pass for keys that are not there
+    const bool infinite = ex == 128;
+    if (infinite) ex = 13;
     if (ex < -100) ex = -100;
-    const float f = __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
+    const float f = infinite ? __builtin_nanf("") : __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
     // scale log2(e) 2^24 / f, kept off 0 and infinity (a masked score is -inf)
     cq[n] = a.scale_log2 * 0x1p11f * __uint_as_float((uint32_t)(127 + ex) << 23);
     cq[n] = fminf(fmaxf(cq[n], 1e-37f), 1e37f);
