@@ -207,7 +207,8 @@ wq_status wq_gemm_noalloc(const void* x, wq_dtype dt, const void* packed, wq_qmo
  *   act      : none, ReLU, SiLU v / (1 + e^-v), or GELU in its tanh form
  *              0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))
  *   residual : device [M][N] in `dt`, or NULL; it may be y itself (the sum is
- *              then formed in place), other overlaps with y are WQ_EINVAL
+ *              then formed in place); other overlaps with y, and any of x or bias
+ *              with y, are WQ_EINVAL (x += layer(x) needs x apart from y)
  * bias and residual are 16-byte aligned.  Other arguments, limits and workspace
  * as for wq_gemv / wq_gemm; the buffer is one from wq_repack (a gate+up layer's
  * columns are interleaved).  Without bias, activation and residual these are
@@ -334,7 +335,8 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  * wq_kv_attention -- out = softmax(scale q K^T) V over the cached values, for
  * prefill, chunks and single tokens alike.
  *   q, out : [rows][q_heads][head_dim] in `dt`, the type of the cache; head h
- *            attends with kv head h / (q_heads / kv_heads); out may be q itself
+ *            attends with kv head h / (q_heads / kv_heads); out may be q itself,
+ *            and shares no element with it otherwise
  *   scale  : positive and finite
  *   causal : 1: a row sees the positions up to its own; 0: its whole sequence
  *   window : > 0: only the last `window` positions up to its own (0: all)

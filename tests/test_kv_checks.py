@@ -213,6 +213,10 @@ def test_epilogue_refusals(L, fn):
     assert epilogue_call(L, fn, res=24) == 2
     assert epilogue_call(L, fn, res=(1 << 20) + 16) == 1           # overlaps y without being y
     assert epilogue_call(L, fn, res=(1 << 20) - 16) == 1
+    assert epilogue_call(L, fn, x=1 << 20) == 1                     # the layer's input as its output
+    assert epilogue_call(L, fn, x=1 << 20, res=1 << 20) == 1        # x += layer(x)
+    assert epilogue_call(L, fn, x=(1 << 20) - 8176) == 1            # x ends 16 bytes into y
+    assert epilogue_call(L, fn, bias=(1 << 20) + 8176) == 1         # bias begins 16 bytes before y's end
     assert epilogue_call(L, fn, x=None) == 1
     assert epilogue_call(L, fn, N=4104) == 2
     assert epilogue_call(L, "wq_gemv_epilogue", M=33) == 2

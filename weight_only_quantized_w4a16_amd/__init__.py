@@ -341,7 +341,7 @@ def wq_gemm(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None)
 def wq_gemv_epilogue(x: torch.Tensor, layer: PackedLayer, bias=None, act=None, residual=None, out=None, ws=None,
                      stream=None) -> torch.Tensor:
     """y = act(x . dequant(W) + bias) + residual for 1 <= M <= 32; act None, "relu", "silu" or "gelu" (tanh form),
-    residual [M][N] (out may be the residual: in place)."""
+    residual [M][N].  out may be the residual (in place), but shares no memory with x or bias."""
     return _product("wq_gemv_epilogue", x, layer, out, ws, stream, (bias, act, residual))
 
 

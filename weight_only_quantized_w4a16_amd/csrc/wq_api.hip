@@ -416,8 +416,11 @@ static wq_status product(bool gemm, bool swiglu, const void* x, wq_dtype dt, con
   if (((uintptr_t)x | (uintptr_t)y | (uintptr_t)packed) & 15) return WQ_EUNSUPPORTED;
   if (((uintptr_t)epi.bias | (uintptr_t)epi.residual) & 15) return WQ_EUNSUPPORTED;
   // the residual is y itself (every element is read where it is written) or apart from it
-  const uintptr_t rb = (uintptr_t)epi.residual, yb = (uintptr_t)y, yn = (uintptr_t)M * N * 2;
-  if (rb && rb != yb && rb < yb + yn && yb < rb + yn) return WQ_EINVAL;
+  const uintptr_t yb = (uintptr_t)y, yn = (uintptr_t)M * N * 2;
+  auto meets_y = [&](const void* p, uintptr_t n) { return p && (uintptr_t)p < yb + yn && yb < (uintptr_t)p + n; };
+  if (epi.residual != y && meets_y(epi.residual, yn)) return WQ_EINVAL;
+  // a layer added to its own input in place would overwrite rows other workgroups still read
+  if (epi.on() && (meets_y(x, (uintptr_t)M * K * 2) || meets_y(epi.bias, (uintptr_t)N * 2))) return WQ_EINVAL;
   if (M > (1 << 24)) return WQ_EUNSUPPORTED;
   if ((size_t)M * K * 2 >= ((size_t)1 << 31)) return WQ_EUNSUPPORTED;  // activation buffer offsets
   const int ksplit = gemm ? gemm_ksplit(M, N, K, bits) : 1;
