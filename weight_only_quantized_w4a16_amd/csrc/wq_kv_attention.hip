@@ -39,7 +39,7 @@
 // rows a wave issues about 490 of them (160 unpack 32 words of codes, which two
 // row tiles share; about nine for each of a lane's 32 scores, one of them the
 // exponential at a quarter of the rate) beside 68 MFMAs of 16 cycles: 4096-row
-// prompts run in 344 us (799 TFLOP/s, vector units 83 % busy, matrix units 33 %).
+// prompts run in 345 us (797 TFLOP/s, vector units 81 % busy, matrix units 34 %).
 // Measured and not kept: three and four row tiles per wave (their sums spill or
 // leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
 // against 137 on 1792 rows of 7 sequences), runs of blocks with and without hidden
