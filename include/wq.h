@@ -346,10 +346,13 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  *            16-byte aligned (may be NULL when 0).  Fewer rows may need more, as
  *            their keys are split further.  Calls that overlap in time must not
  *            share it; nothing in it needs to start at any value
- * A row that sees no position is zero.  Scores, softmax and sums are fp32; the
- * product of a probability and a value step is rounded to fp16 once, and the
- * output to `dt` once.  Value steps s are expected in 2^-60 .. 2^100 (smaller
- * ones lose bits).  The same call gives the same bits.
+ * A row that sees no position is zero.  Scores, softmax and sums are fp32
+ * (scores scale q k are expected within 2^20); the product of a probability and a
+ * value step is rounded to fp16 once, and the output to `dt` once.  That fp16 is
+ * relative to the row's own largest such product over the positions it sees and
+ * all groups: products below 2^-16 of it lose bits (its smallest steps are 2^-26
+ * of it).  Value steps s are expected to be at least 2^-60 (smaller ones lose
+ * bits).  The same call gives the same bits.
  */
 size_t wq_kv_workspace_bytes(int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim,
                              int group, int max_kv_len);

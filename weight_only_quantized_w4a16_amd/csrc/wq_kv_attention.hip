@@ -22,9 +22,15 @@
 //
 // Numbers: q is scaled by a power of two per row so that its largest channel
 // lies in [2^13, 2^14) and converted to fp16 (exact for fp16 and bf16 inputs
-// but for channels 2^-23 below the largest).  P = p s is rounded to fp16 once;
-// its reference is held so that the largest lies near 2^14, so products 2^-24
-// smaller are still normal numbers.  The offsets are added as
+// but for channels 2^-23 below the largest).  P = p s is rounded to fp16 once.
+// What it is relative to is the row's own: set so that the largest p s of the keys
+// it has seen lies at 2^6, and set anew once one may pass 2^15.5.  Every second
+// key's P carries a 2^-4 (its codes the 2^4), so products down to 2^-16 of the
+// row's largest are normal numbers, and half a step of the smallest is 2^-27 of
+// it.  Keys a row does not see, and keys that count for nothing however large
+// their values, have no part in that.  (The room upwards is what keeps the sums
+// from being scaled again and again: 2^10 to 2^14 took 366 us where 2^6 to 2^15.5
+// takes 348.)  The offsets are added as
 // sum P lo / s beside sum P c, from the same rounded P, so that a rounding of P
 // shows times v / s rather than times c: lo / s, as the sum of two fp16, is one
 // more operand tile of the second product (rows 0 and 1 of it).  fp16 outputs,
@@ -62,8 +68,10 @@ namespace wq {
 namespace {
 
 constexpr float kNone = -1e30f;    // reference of a row that has seen no key
-constexpr float kSlack = 8.0f;     // log2 a score may exceed its row's reference by
-constexpr int kStepMin = -60;      // smallest exponent the value steps are referred to
+constexpr float kTop = 6.0f;      // log2 of a row's largest p s when its reference is set
+constexpr float kOver = 15.5f;     // log2 that p s may reach before it is set anew (fp16 ends at 16;
+                                   // scores are good to half of one up to 2^21)
+constexpr float kStepMin = 0x1p-60f;    // references count smaller value steps as this
 constexpr float kStepZero = 0x1p-100f;  // smaller steps (bf16 only) count as none
 
 template <int D, int NG>
@@ -90,6 +98,14 @@ __device__ inline float row_bcast(float v) {
 // compiler's view of what the matrix cores still read.)
 __device__ inline float max3(float a, float b, float c) {
   return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
+// Factor 2^x of a sum of probabilities, in two halves: between keys whose value
+// steps are far apart x may lie below the exponents of fp32 and the product still
+// be one of its numbers.
+__device__ inline float scale_sum(float sum, float x) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * x);
+  return sum * half * half;
 }
 
 // W consecutive words, W = 2, 3, 4, 6 or 8
@@ -266,14 +282,15 @@ void kv_attention_kernel(const KvAttnArgs a) {
   const int nblk = begin < end ? (end - begin + stride - 1) / stride : 0;
 
   f4 acc[NQ][DTL], off[NQ][NG];
-  float ref[NQ], m[NQ], sum[NQ];
-  // the steps of the values seen are at most step_limit = 2^(step_exp + 6)
-  int step_exp = kStepMin;
-  float step_limit = __uint_as_float((uint32_t)(127 + 6 + kStepMin) << 23);
+  // log2 of what a row's probabilities are relative to: kTop below the largest
+  // p s of the keys it has seen, within kOver - kTop
+  float ref[NQ], sum[NQ];
+  // Every block is only asked whether its steps stay below step_limit and its
+  // scores below limit (what p s <= 2^kOver leaves them at such a step).
+  float step_limit = 0.0f, limit[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    m[n] = kNone;
-    ref[n] = kNone + kStepMin;
+    ref[n] = limit[n] = kNone;
     sum[n] = 0.0f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) off[n][g] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -371,7 +388,7 @@ void kv_attention_kernel(const KvAttnArgs a) {
     }
     scored();
     // step and offset / step of this lane's value
-    float vs[NG], smax = 0.0f;
+    float vs[NG], smax = kStepMin;
     uint32_t vr[NG];
     bool nan_value = false;
 #pragma unroll
@@ -389,11 +406,10 @@ void kv_attention_kernel(const KvAttnArgs a) {
       const float r1 = f16_to_f32(f32_to_f16(r));
       vr[g] = pack2<F16>(r1, r - r1);
       nan_value |= st != st;
-      smax = fmaxf(smax, st);
+      smax = st > smax ? st : smax;  // (drops NaN)
       vs[g] = c & 1 ? st * 0x1p-4f : st;
     }
     bool over = smax > step_limit;
-    float top[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       if (edge) {
@@ -411,28 +427,33 @@ void kv_attention_kernel(const KvAttnArgs a) {
 #pragma unroll
       for (int i = 3; i < 15; i += 2) t = max3(t, u[n][i / 4][i % 4], u[n][(i + 1) / 4][(i + 1) % 4]);
       t = max3(t, u[n][3][3], t);
-      top[n] = t * cq[n];
-      over |= top[n] > m[n] + kSlack;
+      over |= t * cq[n] > limit[n];
     }
     if (__any(over)) {
-      // new references: sums so far are brought to them
-      float sx = smax;
+      // The bound on the steps follows this block's, down too: a block of larger
+      // ones costs itself and the next block this pass (half again as much room as
+      // this block needs: 348 us; the next power of two: 352).  New references where
+      // a key the row sees calls for one (a hidden key's score is -inf): sums so far
+      // are brought to them.
+      int sx = __float_as_int(smax);  // positive: ordered as integers
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) sx = fmaxf(sx, __shfl_xor(sx, o, 64));
-      int e = (int)((__float_as_uint(sx) >> 23) & 255) - 127 - 2;  // sx 2^-e in [4, 8)
-      if (e > 120) e = 120;
-      e = __builtin_amdgcn_readfirstlane(e);
-      if (e > step_exp) step_exp = e;
-      step_limit = __uint_as_float((uint32_t)(127 + 6 + step_exp) << 23);
+      for (int o = 1; o < 64; o <<= 1) sx = max(sx, __shfl_xor(sx, o, 64));
+      step_limit = __int_as_float(__builtin_amdgcn_readfirstlane(sx)) * 1.5f;
+      const float step_top = __builtin_amdgcn_logf(step_limit), step = __builtin_amdgcn_logf(smax);  // log2
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float t = fmaxf(top[n], __shfl_xor(top[n], 16, 64));
+        float t = -INFINITY;
+        sfor<16>([&](auto ic) __attribute__((always_inline)) {
+          constexpr int i = decltype(ic)::value;
+          t = fmaxf(t, __builtin_fmaf(u[n][i / 4][i % 4], cq[n], row_bcast<i>(step)));
+        });
+        t = fmaxf(t, __shfl_xor(t, 16, 64));
         t = fmaxf(t, __shfl_xor(t, 32, 64));
-        if (t > m[n]) m[n] = t;
-        const float nref = m[n] + (float)step_exp;
+        const float nref = fmaxf(ref[n], t - kTop);
         const float al = __builtin_amdgcn_exp2f(ref[n] - nref);
+        sum[n] = scale_sum(sum[n], ref[n] - nref);
         ref[n] = nref;
-        sum[n] *= al;
+        limit[n] = nref + (kOver - step_top);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -622,7 +643,7 @@ void kv_attention_kernel(const KvAttnArgs a) {
       f4 v = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        total += ml[(w * BM + x) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(w * BM + x) * 2] - top);
+        total += scale_sum(ml[(w * BM + x) * 2 + 1], ml[(w * BM + x) * 2] - top);
         v += *(const f4*)(od + (w * BM + x) * LDO + d);
       }
       int64_t row;
@@ -670,7 +691,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const KvAttnArgs a) {
     const float al = __builtin_amdgcn_exp2f(r[k] - top);
     // a part that saw no key holds nothing (NaN goes on)
     if (threadIdx.x < 64) weight[lane + 64 * k] = w[k] == 0.0f ? 0.0f : al;
-    total += w[k] * al;
+    total += scale_sum(w[k], r[k] - top);
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o, 64);
@@ -728,7 +749,7 @@ __global__ __launch_bounds__(256) void kv_join_few_kernel(const KvAttnArgs a) {
     if (s >= a.splits || w[s] == 0.0f) continue;  // a part that saw no key (NaN goes on)
     const float al = __builtin_amdgcn_exp2f(r[s] - top);
     const f4 t = *(const f4*)(p + (int64_t)s * all * D);
-    total += w[s] * al;
+    total += scale_sum(w[s], r[s] - top);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(t[i], al, v[i]);
   }
