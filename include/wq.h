@@ -301,6 +301,8 @@ wq_status wq_hadamard(const void* x, wq_dtype dt, void* y, int M, int K, int blo
  * held to 0 .. rows, and positions below 0, past the table (max_pages *
  * page_size) or on a page that is not in 0 .. num_pages - 1 are no place:
  * nothing is written there, they read as zero and attention does not see them.
+ * Attention takes nothing from positions that no row sees either, whatever their
+ * pages hold (before a window, pages need not have been written).
  * Rows outside every sequence (before cu_q[0], from cu_q[batch] on) are left as
  * they were.
  * Row matrices are [rows][heads][head_dim] with heads contiguous and `ld_*`

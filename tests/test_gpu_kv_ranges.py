@@ -1,5 +1,5 @@
 """Attention over the 4-bit cache where the value steps of one call differ by many powers of two: among keys a row does
-not see, among keys that count for nothing, and among those that count alike."""
+not see, among keys that count for nothing, and among those that count alike; and memory that holds anything."""
 import math
 
 import pytest
@@ -192,3 +192,34 @@ def test_scores_far_below_zero(wq, dt):
         # equal probabilities 1 / n: p s rounded to fp16, the output to its type, fp32 sums
         bound = v[seen].abs().mean(0) * 2.0 ** -11 + 8 * 2.0 ** -11 + _kv.EPS[dt] / 2 * (want.abs() + 0.01) + 2.0 ** -15
         assert bool(((got[i] - want).abs() <= bound).all()), i
+
+
+# ---------------------------------------------------------------------------
+# Memory nothing was written to
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("new", [1, 3, 40])
+def test_unwritten_pages_before_the_window(wq, dt, new):
+    """Pages wholly before the window may name a page that was never written: infinite steps and offsets, offsets far
+    larger than their steps, NaN, anything."""
+    inf = 0x7C00 if dt == F16 else 0x7F80
+    big = 0x7BFF if dt == F16 else 0x7F7F
+    n, window = 230, 75
+    first = n - new - window + 1
+    pages = first // 16  # pages before the one the window begins in
+    assert pages % 4  # the block of 64 keys holds a page before the window
+    P = _kv.Problem([n], [new], 1, 64, 64, 16, dt, 60 + new)
+    q = P.queries(2)
+    want, bound = reference(q, P.K[0], P.V[0], torch.arange(n - new, n), 0.125, 64, window=window)
+    for s, lo in ((inf, inf), (inf, 0), (1, big), (1, big | 0x8000), (0x3C00, inf), (0x8001, inf | 0x8000), (0xFFFF, 0xFFFF)):
+        cache = P.empty(wq)
+        P.fill(wq, cache)
+        word = (s | lo << 16)
+        word -= (word >> 31) << 32
+        spare = P.free[0]
+        per = cache.data.numel() // P.num_pages
+        cache.data[spare * per:(spare + 1) * per].view(torch.int32).fill_(word)
+        table = P.table.clone()
+        table[0, :pages] = spare
+        got = wq.wq_kv_attention(q.cuda(), cache, table.cuda(), i32([n]), scale=0.125, window=window).cpu().double()
+        assert worst((got - want).abs(), bound) <= 1, (hex(s), hex(lo))

@@ -393,8 +393,10 @@ void kv_attention_kernel(const KvAttnArgs a) {
     bool nan_value = false;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      // values of keys that are not there count as zero whatever the memory holds
-      const uint32_t m = rec < 0 || kl + c >= sq.len ? 0u : f.vm[g];
+      // values of keys that are not there, or that no row of the wave sees (pages
+      // before a window may never have been written), count as zero whatever the
+      // memory holds
+      const uint32_t m = rec < 0 || (uint32_t)(kl + c - lo_min) >= (uint32_t)(hi_max - lo_min) ? 0u : f.vm[g];
       const float l = act_hi<DT>(m);
       float st = act_lo<DT>(m);
       if (st < kStepZero) st = fabsf(l);  // NaN for a group of NaN
