@@ -1,5 +1,6 @@
-"""Attention over the 4-bit cache where the value steps of one call differ by many powers of two: among keys a row does
-not see, among keys that count for nothing, and among those that count alike; and memory that holds anything."""
+"""Attention over the 4-bit cache where steps of one call differ by many powers of two -- values of keys a row does not
+see, of keys that count for nothing, of keys that count alike; key groups far below the others -- and where memory that
+no row sees holds anything."""
 import math
 
 import pytest
@@ -223,3 +224,30 @@ def test_unwritten_pages_before_the_window(wq, dt, new):
         table[0, :pages] = spare
         got = wq.wq_kv_attention(q.cuda(), cache, table.cuda(), i32([n]), scale=0.125, window=window).cpu().double()
         assert worst((got - want).abs(), bound) <= 1, (hex(s), hex(lo))
+
+
+# ---------------------------------------------------------------------------
+# Key steps
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("e", [-40, -90, -101, -110, -120, -128])
+@pytest.mark.parametrize("D,G,new", [(64, 64, 1), (64, 32, 1), (64, 32, 40), (128, 128, 40), (128, 64, 3)])
+def test_tiny_key_groups(wq, e, D, G, new):
+    """A group of keys far below the others adds next to nothing to a score, down to the subnormals of the type."""
+    P = _kv.Problem([150], [new], 1, D, G, 16, BF16, e + 200 + D)
+    P.K[0][:, :, :G] = (P.K[0][:, :, :G].double() * 2.0 ** e).to(BF16)
+    q = P.queries(2)
+    got = run(wq, P, q)
+    want, bound = reference(q, P.K[0], P.V[0], torch.arange(150 - new, 150), D ** -0.5, G)
+    assert worst((got - want).abs(), bound) <= 1
+
+
+@pytest.mark.parametrize("e", [90, 97, 104])
+@pytest.mark.parametrize("new", [1, 40])
+def test_tiny_keys_meet_large_queries(wq, e, new):
+    """Keys around 2^-e and queries around 2^e: ordinary scores."""
+    P = _kv.Problem([150], [new], 1, 64, 64, 16, BF16, e)
+    P.K[0] = (P.K[0].double() * 2.0 ** -e).to(BF16)
+    q = (P.queries(2).double() * 2.0 ** e).to(BF16)
+    got = run(wq, P, q)
+    want, bound = reference(q, P.K[0], P.V[0], torch.arange(150 - new, 150), 0.125, 64)
+    assert worst((got - want).abs(), bound) <= 1

@@ -72,7 +72,7 @@ constexpr float kTop = 6.0f;      // log2 of a row's largest p s when its refere
 constexpr float kOver = 15.5f;     // log2 that p s may reach before it is set anew (fp16 ends at 16;
                                    // scores are good to half of one up to 2^21)
 constexpr float kStepMin = 0x1p-60f;    // references count smaller value steps as this
-constexpr float kStepZero = 0x1p-100f;  // smaller steps (bf16 only) count as none
+constexpr float kStepZero = 0x1p-100f;  // smaller value steps (bf16 only) count as none
 
 template <int D, int NG>
 struct KvBlock {  // one lane's share of a block of 64 keys
@@ -339,9 +339,11 @@ void kv_attention_kernel(const KvAttnArgs a) {
     for (int g = 0; g < NG; ++g) {
       ks[g] = act_lo<DT>(f.km[g]);
       kr[g] = act_hi<DT>(f.km[g]);
-      const bool flat = ks[g] < kStepZero;
-      ks[g] = flat ? 1.0f : ks[g];
-      kr[g] *= flat ? 1.0f : __builtin_amdgcn_rcpf(ks[g]);
+      // a group without a step (its codes are 0) takes 1 for one; the subnormals of
+      // bf16 count as its smallest normal number, whose reciprocal is one too
+      const bool flat = ks[g] == 0.0f;
+      ks[g] = flat ? 1.0f : fmaxf(ks[g], 0x1p-126f);
+      kr[g] *= __builtin_amdgcn_rcpf(ks[g]);
     }
     // scores: keys x rows
     f4 u[NQ][4];
