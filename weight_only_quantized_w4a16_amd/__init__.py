@@ -104,13 +104,17 @@ def _stream(stream, dev: torch.device) -> int:
     return stream.cuda_stream
 
 
-def _used_on(stream, *tensors):
-    """Tensors this package allocates come from the current stream's memory.  Work given to another stream must keep
-    them from being handed out again before it is done with them."""
-    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(stream.device_index):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _empty(stream, shape, dtype: torch.dtype, dev: torch.device, scratch: bool = False) -> torch.Tensor:
+    """Memory for work on `stream` (the current one by default).  It comes from that stream's own: memory of the
+    current stream may still be in use there by work its last owner left behind, which another stream does not wait
+    for.  What the caller gets (not scratch) is also kept for what the current stream does with it."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _check(fn: str, rc: int):
@@ -213,16 +217,17 @@ def _repack(fn: str, qweight, scales, zeros, mode, g_idx, K, N, bits, group_size
     nbytes = wq_packed_bytes(K, N, bits, group_size, mode)
     if nbytes == 0:
         raise WQError("wq_packed_bytes", 2)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    at = _stream(stream, dev)
+    packed = _empty(stream, nbytes, torch.uint8, dev)
     perm = None
     g_host = None
     if g_idx is not None:
         import numpy as np
         g_host = np.ascontiguousarray(torch.as_tensor(g_idx).cpu().numpy(), dtype=np.int32)
-        perm = torch.empty(K, dtype=torch.int32, device=dev)
+        perm = _empty(stream, K, torch.int32, dev)
     rc = getattr(lib(), fn)(_ptr(qweight), _ptr(scales), _ptr(zeros), mode,
                             None if g_host is None else ctypes.c_void_p(g_host.ctypes.data),
-                            K, N, bits, group_size, _ptr(packed), _ptr(perm), _stream(stream, dev))
+                            K, N, bits, group_size, _ptr(packed), _ptr(perm), at)
     _check(fn, rc)
     return PackedLayer(packed, K, N, bits, group_size, mode, lut, perm, fn == "wq_repack_gate_up")
 
@@ -268,10 +273,10 @@ def wq_dequant_debug(layer: PackedLayer, dtype: torch.dtype, stream=None) -> tor
     _dt(dtype)
     _check_layer(layer, layer.packed.device)
     _check_cuda(layer.packed, "layer.packed")
-    w = torch.empty((layer.K, layer.N), dtype=dtype, device=layer.packed.device)
+    at = _stream(stream, layer.packed.device)
+    w = _empty(stream, (layer.K, layer.N), dtype, layer.packed.device)
     rc = lib().wq_dequant_debug(_ptr(layer.packed), layer.mode, _ptr(layer.lut), _ptr(layer.perm),
-                                layer.K, layer.N, layer.bits, layer.group_size, _dt(dtype), _ptr(w),
-                                _stream(stream, w.device))
+                                layer.K, layer.N, layer.bits, layer.group_size, _dt(dtype), _ptr(w), at)
     _check("wq_dequant_debug", rc)
     return w
 
@@ -313,18 +318,16 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
         _need(ws.numel() * ws.element_size() >= need, lambda: f"ws holds fewer than the {need} bytes this call needs")
     _check_layer(layer, dev)
     _check_cuda(x, "x")
-    new_out = new_ws = None
+    at = _stream(stream, dev)
     if out is None:
-        out = new_out = x.new_empty((M, ncols))
+        out = _empty(stream, (M, ncols), x.dtype, dev)
     if need and ws is None:
-        ws = new_ws = x.new_empty(need, dtype=torch.uint8)
+        ws = _empty(stream, need, torch.uint8, dev, scratch=True)
     rc = getattr(L, fn)(x.data_ptr(), dt, layer.packed.data_ptr(), layer.mode, _ptr(layer.lut), _ptr(layer.perm),
                         *extra, out.data_ptr(), M, layer.N, layer.K, layer.bits, layer.group_size,
-                        ws.data_ptr() if need else None, need, _stream(stream, dev))
+                        ws.data_ptr() if need else None, need, at)
     if rc:
         raise WQError(fn, rc)
-    if stream is not None:
-        _used_on(stream, new_out, new_ws)
     return out
 
 
@@ -389,12 +392,14 @@ def wq_hadamard(x: torch.Tensor, block: int, out: Optional[torch.Tensor] = None,
         raise ValueError("x must be a contiguous [M][K] tensor")
     M, K = x.shape
     _dt(x.dtype)
-    if out is None:
-        out = torch.empty_like(x)
-    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous() or out.device != x.device:
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous()
+                            or out.device != x.device):
         raise ValueError("out must be a contiguous tensor like x, on its device")
     _check_cuda(x, "x")
-    rc = lib().wq_hadamard(_ptr(x), _dt(x.dtype), _ptr(out), M, K, block, _stream(stream, x.device))
+    at = _stream(stream, x.device)
+    if out is None:
+        out = _empty(stream, (M, K), x.dtype, x.device)
+    rc = lib().wq_hadamard(_ptr(x), _dt(x.dtype), _ptr(out), M, K, block, at)
     _check("wq_hadamard", rc)
     return out
 

@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import WQError, _check_cuda, _check_tensor, _dt, _need, _ptr, _stream, _used_on, lib
+from . import WQError, _check_cuda, _check_tensor, _dt, _empty, _need, _ptr, _stream, lib
 
 
 @dataclasses.dataclass(frozen=True)
@@ -142,23 +142,21 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
     if not (isinstance(rows, int) and rows >= 0):
         raise ValueError("rows must be a count")
     batch, max_pages = _check_seqs(dev, block_table, kv_lens, cu_q, rows)
-    if out is None:
-        k = torch.empty((rows, cache.kv_heads, cache.head_dim), dtype=cache.dtype, device=dev)
-        v = torch.empty_like(k)
-        new = (k, v)
-    else:
-        new = ()
+    if out is not None:
         k, v = out
-    k_at, ld_k = _check_rows(k, "out[0]", cache, dev, cache.kv_heads, rows)
-    v_at, ld_v = _check_rows(v, "out[1]", cache, dev, cache.kv_heads, rows)
+        k_at, ld_k = _check_rows(k, "out[0]", cache, dev, cache.kv_heads, rows)
+        v_at, ld_v = _check_rows(v, "out[1]", cache, dev, cache.kv_heads, rows)
     _check_cuda(data, "cache.data")
+    at = _stream(stream, dev)
+    if out is None:
+        k, v = (_empty(stream, (rows, cache.kv_heads, cache.head_dim), cache.dtype, dev) for _ in range(2))
+        k_at, v_at, ld_k = k.data_ptr(), v.data_ptr(), cache.kv_heads * cache.head_dim
+        ld_v = ld_k
     rc = lib().wq_kv_read(data.data_ptr(), k_at, v_at, ld_k, ld_v, cache.dt, block_table.data_ptr(),
                           kv_lens.data_ptr(), _ptr(cu_q), rows, batch, max_pages, cache.num_pages, cache.page_size,
-                          cache.kv_heads, cache.head_dim, cache.group, _stream(stream, dev))
+                          cache.kv_heads, cache.head_dim, cache.group, at)
     if rc:
         raise WQError("wq_kv_read", rc)
-    if stream is not None:
-        _used_on(stream, *new)
     return k, v
 
 
@@ -211,18 +209,16 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     if out is not None:
         o_at, ld_o = _check_rows(out, "out", cache, dev, q_heads, rows)
     _check_cuda(data, "cache.data")
-    new_out = new_ws = None
+    at = _stream(stream, dev)
     if out is None:
-        out = new_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty(stream, (rows, q_heads, cache.head_dim), cache.dtype, dev)
         o_at, ld_o = out.data_ptr(), q_heads * cache.head_dim
     if need and ws is None:
-        ws = new_ws = data.new_empty(need)
+        ws = _empty(stream, need, torch.uint8, dev, scratch=True)
     rc = L.wq_kv_attention(q_at, ld_q, cache.dt, data.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
                            _ptr(cu_q), o_at, ld_o, rows, batch, max_pages, cache.num_pages, cache.page_size, q_heads,
                            cache.kv_heads, cache.head_dim, cache.group, scale, 1 if causal else 0, window, max_kv_len,
-                           ws.data_ptr() if need else None, need, _stream(stream, dev))
+                           ws.data_ptr() if need else None, need, at)
     if rc:
         raise WQError("wq_kv_attention", rc)
-    if stream is not None:
-        _used_on(stream, new_out, new_ws)
     return out

@@ -30,7 +30,7 @@ from typing import List, Optional
 import torch
 
 from . import (KVCache, PackedLayer, linear, use_gemv, wq_gemm, wq_gemm_gate_up, wq_gemv, wq_gemv_gate_up,
-               _used_on, wq_kv_attention, wq_kv_cache, wq_kv_workspace_bytes, wq_kv_write)
+               _empty, wq_kv_attention, wq_kv_cache, wq_kv_workspace_bytes, wq_kv_write)
 
 
 @dataclasses.dataclass
@@ -151,7 +151,7 @@ class CachedStack:
         need = wq_kv_workspace_bytes(T, batch, ragged, H, KV, D, self.caches[0].group,
                                      block_table.shape[1] * self.caches[0].page_size if max_kv_len is None
                                      else max_kv_len)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        ws = _empty(stream, need, torch.uint8, x.device, scratch=True) if need else None
         cur = x
         for i, (L, cache) in enumerate(zip(self.layers, self.caches)):
             linear(cur, L.qkv, out=qkv, stream=stream, bias=None if self.bias is None else self.bias[i])
@@ -166,5 +166,4 @@ class CachedStack:
                 record.append(dict(layer=i, x=cur.clone(), qkv=qkv.clone(), attn=attn.clone(), mid=mid.clone(),
                                    h=h.clone(), y=nxt.clone()))
             cur = nxt
-        _used_on(stream, ws)
         return cur
