@@ -178,3 +178,41 @@ def test_stack_refusals(wq, weights):
     st = make_stack(weights, 2)
     with pytest.raises(ValueError, match="max_rows"):
         st.step(torch.zeros(3, DIM, dtype=torch.float16, device="cuda"), i32([[0]]), i32([3]))
+
+
+def test_record_on_another_stream(wq, weights):
+    """The recorded tensors are copied where the work is: a step given to a busy stream records what it computes, and
+    its input also where the layer writes its output over it."""
+    from weight_only_quantized_w4a16_amd.stack import CachedStack, DecodeStack, DecoderWeights
+    layers, raw, bias = weights
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(3, DIM, generator=g).half().cuda()
+    table, lens = i32([[0], [1], [2]]), i32([1, 1, 1])
+    # (the chain without a cache takes the first columns of its QKV output into a projection of DIM columns)
+    plain = [DecoderWeights(layers[0].qkv, layers[0].o, layers[0].gate_up, layers[0].down)]
+    cached = CachedStack(layers[:1], H, KV, D, 8, 3, torch.float16, "cuda", qkv_bias=bias[:1])
+    side = torch.cuda.Stream()
+    a = torch.randn(4096, 4096, device="cuda").half()
+    b = torch.empty_like(a)
+    for st, args in ((cached, (table, lens)), (DecodeStack(plain, 3, torch.float16, "cuda"), ())):
+        want = []
+        y = st.step(x, *args, record=want).clone()
+        again = []
+        st.step(st.step(x, *args), *args, record=again)  # its own output buffer as the input
+        torch.cuda.synchronize()
+        assert torch.equal(again[0]["x"], y)
+        assert torch.equal(want[0]["y"], y) and torch.equal(want[0]["x"], x)
+        for t in vars(st).values():
+            for buf in t if isinstance(t, list) else [t]:
+                if isinstance(buf, torch.Tensor) and buf.dtype == torch.float16 and buf.is_cuda and buf.shape[-1] != QKV:
+                    buf.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                torch.mm(a, a, out=b)
+        rec = []
+        st.step(x, *args, stream=side, record=rec)
+        side.synchronize()
+        assert rec[0].keys() == want[0].keys() and rec[0]["layer"] == 0
+        for name, t in want[0].items():
+            assert name == "layer" or torch.equal(rec[0][name], t), name

@@ -42,6 +42,16 @@ class DecoderWeights:
     down: PackedLayer      # [inter] -> [dim]
 
 
+def _copies(stream, **tensors) -> dict:
+    """Clones made on `stream` (the current one by default), where the work that fills the tensors is."""
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        copies = {name: t.clone() for name, t in tensors.items()}
+    for t in copies.values():
+        t.record_stream(here)
+    return copies
+
+
 class DecodeStack:
     """y = layer_L-1( ... layer_0(x)) with layer(x) = down(SiLU(gate(o(qkv(x)[:, :dim]))) * up(...))."""
 
@@ -79,6 +89,8 @@ class DecodeStack:
             raise ValueError("x must be a contiguous [M][dim] tensor")
         cur = x
         for i, L in enumerate(self.layers):
+            if record is not None:  # (the layer's output may be written over its input)
+                record.append(dict(layer=i, **_copies(stream, x=cur)))
             self._lin(cur, L.qkv, out=self.qkv_out, stream=stream)
             if self.M == 1:
                 attn = self.qkv_out[:, :self.dim]  # a contiguous prefix of the single row
@@ -91,8 +103,7 @@ class DecodeStack:
             nxt = self.x[i % 2]
             self._lin(self.h, L.down, out=nxt, stream=stream)
             if record is not None:
-                record.append(dict(layer=i, x=cur.clone(), qkv=self.qkv_out.clone(), attn=attn.clone(),
-                                   o=self.o_out.clone(), h=self.h.clone(), y=nxt.clone()))
+                record[-1].update(_copies(stream, qkv=self.qkv_out, attn=attn, o=self.o_out, h=self.h, y=nxt))
             cur = nxt
         return cur
 
@@ -154,6 +165,8 @@ class CachedStack:
         ws = _empty(stream, need, torch.uint8, x.device, scratch=True) if need else None
         cur = x
         for i, (L, cache) in enumerate(zip(self.layers, self.caches)):
+            if record is not None:  # (the layer's output may be written over its input)
+                record.append(dict(layer=i, **_copies(stream, x=cur)))
             linear(cur, L.qkv, out=qkv, stream=stream, bias=None if self.bias is None else self.bias[i])
             wq_kv_write(k, v, cache, block_table, kv_lens, cu_q, stream=stream)
             wq_kv_attention(q, cache, block_table, kv_lens, cu_q, window=window, max_kv_len=max_kv_len, out=attn,
@@ -163,7 +176,6 @@ class CachedStack:
             nxt = self.x[i % 2][:T]
             linear(h, L.down, out=nxt, stream=stream, residual=mid)
             if record is not None:
-                record.append(dict(layer=i, x=cur.clone(), qkv=qkv.clone(), attn=attn.clone(), mid=mid.clone(),
-                                   h=h.clone(), y=nxt.clone()))
+                record[-1].update(_copies(stream, qkv=qkv, attn=attn, mid=mid, h=h, y=nxt))
             cur = nxt
         return cur
