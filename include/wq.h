@@ -326,7 +326,8 @@ wq_status wq_kv_write(const void* k, const void* v, int64_t ld_k, int64_t ld_v, 
 
 /*
  * wq_kv_read -- the cached values lo + s c of the rows' places, rounded to
- * `dt` (the type they were written in) once.
+ * `dt` (the type they were written in) once.  k and v share no element
+ * (WQ_EINVAL).
  */
 wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t ld_v, wq_dtype dt,
                      const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_q, int rows, int batch,
@@ -337,8 +338,8 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  * wq_kv_attention -- out = softmax(scale q K^T) V over the cached values, for
  * prefill, chunks and single tokens alike.
  *   q, out : [rows][q_heads][head_dim] in `dt`, the type of the cache; head h
- *            attends with kv head h / (q_heads / kv_heads); out may be q itself,
- *            and shares no element with it otherwise
+ *            attends with kv head h / (q_heads / kv_heads); out may be q itself
+ *            (with its stride), other shared elements are WQ_EINVAL
  *   scale  : positive and finite
  *   causal : 1: a row sees the positions up to its own; 0: its whole sequence
  *   window : > 0: only the last `window` positions up to its own (0: all)

@@ -470,6 +470,30 @@ def test_attention_strided(wq):
     assert bool((o[:, :128] == 9).all()) and bool((o[:, 5 * 128:] == 9).all())
 
 
+@pytest.mark.parametrize("lens,new,max_kv", [([90, 33], [1, 1], None), ([300], [80], None), ([3000], [1], None)])
+def test_attention_beside_its_queries(wq, lens, new, max_kv):
+    """Queries and outputs as slices of one buffer's rows, either first; over each other they are refused."""
+    P = _kv.Problem(lens, new, 2, 64, 64, 16, F16, 32)
+    cache = P.empty(wq)
+    P.fill(wq, cache)
+    q = P.queries(4)
+    want, bound = P.reference(q, 0.125)
+    for at_q, at_o in ((0, 4), (4, 0)):
+        wide = torch.full((sum(new), 8, 64), 9.0, dtype=F16, device="cuda")
+        wide[:, at_q:at_q + 4] = q.cuda()
+        out = wide[:, at_o:at_o + 4]
+        wq.wq_kv_attention(wide[:, at_q:at_q + 4], cache, P.table.cuda(), i32(lens), out=out, max_kv_len=max_kv)
+        assert bool(((out.cpu().double() - want).abs() <= bound).all())
+        assert torch.equal(wide[:, at_q:at_q + 4].cpu(), q)
+        with pytest.raises(wq.WQError) as e:
+            wq.wq_kv_attention(wide[:, 1:5], cache, P.table.cuda(), i32(lens), out=wide[:, 2:6], max_kv_len=max_kv)
+        assert e.value.status == 1
+    k = torch.zeros(sum(new), 2, 64, dtype=F16, device="cuda")
+    with pytest.raises(wq.WQError) as e:
+        wq.wq_kv_read(cache, P.table.cuda(), i32(lens), sum(new), out=(k, k))
+    assert e.value.status == 1
+
+
 def test_attention_of_rotated_rows(wq):
     """Queries and keys rotated head by head (wq_hadamard) before they are cached: the same attention, with an outlier
     channel spread over its group."""

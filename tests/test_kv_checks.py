@@ -106,6 +106,34 @@ def test_workspace_bytes(L):
     assert one % (8 * (128 + 2) * 4) == 0 and 2 <= one // (8 * (128 + 2) * 4) <= 128
 
 
+def meets(a, ld_a, b, ld_b, rows, width):
+    """Whether two row matrices share an element, by counting (addresses in bytes)."""
+    e = {a // 2 + i * ld_a + j for i in range(rows) for j in range(width)}
+    return any(b // 2 + i * ld_b + j in e for i in range(rows) for j in range(width))
+
+
+def test_shared_rows_are_refused(L):
+    """Outputs over other rows' inputs, or over each other, are refused, slices that lie between each other's rows are
+    not.  (Pointers are never read: what is not refused for its overlap ends at the missing workspace.)"""
+    base, width = 1 << 20, 8 * 64
+    for rows, ld_q, ld_out in ((2, 512, 512), (2, 1536, 1536), (4, 1024, 1024), (3, 1536, 1024), (3, 520, 1032), (1, 512, 512)):
+        for d in sorted({i * 8 + o for i in (-3 * 192, -2 * 192, -192, -129, -128, -65, -64, -63, 0, 63, 64, 65, 128, 192)
+                         for o in (-8, 0, 8)}):
+            out = base + 2 * d
+            shared = meets(base, ld_q, out, ld_out, rows, width) and not (d == 0 and (rows == 1 or ld_q == ld_out))
+            assert attend_call(L, q=base, ld_q=ld_q, out=out, ld_out=ld_out, rows=rows, batch=rows, D=64, G=64, q_heads=8,
+                               max_kv=100000) == (1 if shared else 4), (rows, ld_q, ld_out, d)
+    # a long matrix with rows between the other's, strides that differ, and strides no memory has
+    assert attend_call(L, q=base, out=base + 2 * 512 * 5, ld_q=1024, ld_out=512, rows=1 << 14, batch=1 << 14, D=64, G=64,
+                       q_heads=8) == 1
+    assert attend_call(L, q=base, out=base + 16, ld_q=1 << 62, ld_out=1 << 61, D=64, G=64, q_heads=8) == 1
+    assert attend_call(L, q=base, out=base + 1024, ld_q=1 << 62, ld_out=1 << 61, D=64, G=64, q_heads=8, max_kv=100000) == 4
+    # keys and values read back over each other
+    for v, ld_k, ld_v in ((base, 512, 512), (base + 2 * 504, 512, 512), (base - 2 * 504, 512, 512), (base + 2 * 512, 512, 512),
+                          (base + 2 * 520, 1024, 1024), (base + 1024, 1024, 512)):
+        assert rows_call(L, "wq_kv_read", k=base, v=v, ld_k=ld_k, ld_v=ld_v) == 1, (v, ld_k, ld_v)
+
+
 @pytest.fixture(scope="module")
 def cache(L):
     return wq.wq_kv_cache(4, 16, 2, 64, 64, torch.float16, device="cpu")
