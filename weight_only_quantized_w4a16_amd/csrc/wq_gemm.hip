@@ -55,7 +55,10 @@ struct GemmArgs {
 // memory operations are outstanding and leaves the other counters alone.
 constexpr int vmcnt_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
 
-template <int DT, int BITS, int MODE, int GPU, bool EPI_SCALE, int BM, int NT>
+// TAIL: the epilogue product's kernel, a form of its own.  As a branch of the
+// plain kernel its code cost the plain products up to 8 registers and 0.3 to
+// 1.4 % (2-bit 4096-row layers 1 %) of their time.
+template <int DT, int BITS, int MODE, int GPU, bool EPI_SCALE, int BM, int NT, bool TAIL>
 __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
   constexpr int BN = 64 * NT;         // NT 16-column tiles per wave, four waves
   constexpr int KT = BITS == 2 ? 256 : 128;
@@ -340,55 +343,57 @@ __global__ __launch_bounds__(256, 2) void gemm_kernel(const GemmArgs a) {
     }
   };
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-  if (a.ksplit > 1) {
-    // Split K: this workgroup's fp32 partial sums (scaled when the scale sits
-    // in the epilogue) go to its slice of the workspace; the reduction kernel
-    // adds the slices in split order and applies the output stage.
-    float* dst = a.part + (size_t)ks * a.M * a.N;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (nt0 + t >= a.ntiles) continue;
-      const int n = (nt0 + t) * 16 + 4 * h;
-      float s[4];
-      col_scales(t, s);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = m0 + 16 * i + c;
-        if (m < a.M)
-          *(f4*)(dst + (size_t)m * a.N + n) =
-              f4{acc[i][t][0] * s[0], acc[i][t][1] * s[1], acc[i][t][2] * s[2], acc[i][t][3] * s[3]};
-      }
-    }
-    return;
-  }
-  if (a.swiglu) {
-    // Fused gate+up layer: column tiles are interleaved (gate, up, ...), so
-    // tiles 2p and 2p + 1 of the wave are the gate and up halves of output
-    // tile nt0 / 2 + p (nt0 is a multiple of 4 and the tile count even).
-#pragma unroll
-    for (int p = 0; p < NT / 2; ++p) {
-      if (nt0 + 2 * p >= a.ntiles) continue;
-      float sg[4], su[4];
-      col_scales(2 * p, sg);
-      col_scales(2 * p + 1, su);
-      const int n = (nt0 / 2 + p) * 16 + 4 * h;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int m = m0 + 16 * i + c;
-        if (m < a.M) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float g = acc[i][2 * p][e] * sg[e];
-            v[e] = g / (1.0f + expf(-g)) * (acc[i][2 * p + 1][e] * su[e]);
-          }
-          *(u32x2*)(a.y + (size_t)m * (a.N / 2) + n) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+  if constexpr (!TAIL) {
+    if (a.ksplit > 1) {
+      // Split K: this workgroup's fp32 partial sums (scaled when the scale sits
+      // in the epilogue) go to its slice of the workspace; the reduction kernel
+      // adds the slices in split order and applies the output stage.
+      float* dst = a.part + (size_t)ks * a.M * a.N;
+  #pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (nt0 + t >= a.ntiles) continue;
+        const int n = (nt0 + t) * 16 + 4 * h;
+        float s[4];
+        col_scales(t, s);
+  #pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int m = m0 + 16 * i + c;
+          if (m < a.M)
+            *(f4*)(dst + (size_t)m * a.N + n) =
+                f4{acc[i][t][0] * s[0], acc[i][t][1] * s[1], acc[i][t][2] * s[2], acc[i][t][3] * s[3]};
         }
       }
+      return;
     }
-    return;
+    if (a.swiglu) {
+      // Fused gate+up layer: column tiles are interleaved (gate, up, ...), so
+      // tiles 2p and 2p + 1 of the wave are the gate and up halves of output
+      // tile nt0 / 2 + p (nt0 is a multiple of 4 and the tile count even).
+  #pragma unroll
+      for (int p = 0; p < NT / 2; ++p) {
+        if (nt0 + 2 * p >= a.ntiles) continue;
+        float sg[4], su[4];
+        col_scales(2 * p, sg);
+        col_scales(2 * p + 1, su);
+        const int n = (nt0 / 2 + p) * 16 + 4 * h;
+  #pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int m = m0 + 16 * i + c;
+          if (m < a.M) {
+            float v[4];
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float g = acc[i][2 * p][e] * sg[e];
+              v[e] = g / (1.0f + expf(-g)) * (acc[i][2 * p + 1][e] * su[e]);
+            }
+            *(u32x2*)(a.y + (size_t)m * (a.N / 2) + n) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+          }
+        }
+      }
+      return;
+    }
   }
-  if (a.epi.on) {
+  if constexpr (TAIL) {
     // Everything to be added is loaded before anything is stored (the residual
     // may be y, so no load could move above a store): the registers of the
     // products' operands are free by now.
@@ -560,15 +565,21 @@ wq_status run_gemm(GemmArgs g, hipStream_t s) {
   g.mtiles = (g.M + bm - 1) / bm;
   g.ktps = (g.ktiles + g.ksplit - 1) / g.ksplit;
   const int grid = g.mtiles * g.ntiles_wg * g.ksplit;
-  if (bm == 64) {
-    if constexpr (!NO64)
-      hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 64, 4>), dim3(grid), dim3(256), 0, s, g);
-  } else if (nt == 2) {
-    hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 128, 2>), dim3(grid), dim3(256), 0, s, g);
-  } else {
-    if constexpr (FIT128)
-      hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 128, 4>), dim3(grid), dim3(256), 0, s, g);
-  }
+  auto launch = [&](auto tail) {
+    constexpr bool TAIL = decltype(tail)::value;
+    if (bm == 64) {
+      if constexpr (!NO64)
+        hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 64, 4, TAIL>), dim3(grid), dim3(256), 0, s, g);
+    } else if (nt == 2) {
+      hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 128, 2, TAIL>), dim3(grid), dim3(256), 0, s, g);
+    } else {
+      if constexpr (FIT128)
+        hipLaunchKernelGGL((gemm_kernel<DT, BITS, MODE, GPU, EPI, 128, 4, TAIL>), dim3(grid), dim3(256), 0, s, g);
+    }
+  };
+  // (with K split the reduction has the epilogue)
+  if (g.epi.on && g.ksplit == 1) launch(std::true_type{});
+  else launch(std::false_type{});
   if (g.ksplit > 1) {
     const size_t quads = (size_t)g.M * (g.swiglu ? g.N / 2 : g.N) / 4;
     int rows = 1;  // threads per group of 4 outputs: about 2^18 threads in all
