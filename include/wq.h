@@ -350,7 +350,7 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  *            their keys are split further.  Calls that overlap in time must not
  *            share it; nothing in it needs to start at any value
  * A row that sees no position is zero.  Scores, softmax and sums are fp32
- * (scores scale q k are expected within 2^20); the product of a probability and a
+ * (scores scale q k are expected within 2^25); the product of a probability and a
  * value step is rounded to fp16 once, and the output to `dt` once.  That fp16 is
  * relative to the row's own largest such product over the positions it sees and
  * all groups: products below 2^-16 of it lose bits (its smallest steps are 2^-26

@@ -251,3 +251,34 @@ def test_tiny_keys_meet_large_queries(wq, e, new):
     got = run(wq, P, q)
     want, bound = reference(q, P.K[0], P.V[0], torch.arange(150 - new, 150), 0.125, 64)
     assert worst((got - want).abs(), bound) <= 1
+
+
+# ---------------------------------------------------------------------------
+# Scores
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [2.0 ** -6, 0.25, 1.0])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_beyond_the_fraction_of_fp32(wq, new, scale, sign):
+    """Scores of 2^24 scale, where fp32 holds whole numbers at best: a later block's scores lie above the first one's
+    by anything between nothing and all, and the output stays between the two blocks' values, at the second's where
+    that has the weight whichever way the scores are rounded (each by up to 2^-22 of itself: the dot product's sums
+    and the product with scale log2 e)."""
+    n = 128 + 40
+    off = 2.0 ** -22 * 2.0 ** 24 * scale * 2
+    for step in [0.0] + [2.0 ** e * m for e in range(0, 6) for m in (1.0, 1.5)]:
+        P = _kv.Problem([n], [new], 1, 64, 32, 16, F16, 1)
+        P.K[0] = torch.zeros(n, 1, 64, dtype=F16)
+        P.K[0][:, :, :32] = 8192.0 * sign      # groups of equal channels: held exactly
+        P.K[0][64:, :, 32:] = step / scale
+        P.V[0] = torch.linspace(1, 2, 64).half().repeat(n, 1, 1)
+        P.V[0][64:] += 4
+        q = torch.zeros(new, 2, 64, dtype=F16)
+        q[:, :, 0], q[:, :, 32] = 2048.0, 1.0
+        got = run(wq, P, q, scale=scale)
+        a, b = (_kv.stored(P.V[0], 32)[i, 0].double() for i in (0, 64))
+        tol = 8 * 2.0 ** -10
+        assert bool(got.isfinite().all()), step
+        assert bool(((got >= a - tol) & (got <= b + tol)).all()), step
+        if step - off > 12:
+            assert bool(((got - b).abs() <= tol + 4 * 64 * math.exp(-12)).all()), step

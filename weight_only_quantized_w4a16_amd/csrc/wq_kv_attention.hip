@@ -69,8 +69,7 @@ namespace {
 
 constexpr float kNone = -1e30f;    // reference of a row that has seen no key
 constexpr float kTop = 6.0f;      // log2 of a row's largest p s when its reference is set
-constexpr float kOver = 15.5f;     // log2 that p s may reach before it is set anew (fp16 ends at 16;
-                                   // scores are good to half of one up to 2^21)
+constexpr float kOver = 15.5f;     // log2 that p s may reach before it is set anew (fp16 ends at 16)
 constexpr float kStepMin = 0x1p-60f;    // references count smaller value steps as this
 constexpr float kStepZero = 0x1p-100f;  // smaller value steps (bf16 only) count as none
 
@@ -457,7 +456,8 @@ void kv_attention_kernel(const KvAttnArgs a) {
         const float al = __builtin_amdgcn_exp2f(ref[n] - nref);
         sum[n] = scale_sum(sum[n], ref[n] - nref);
         ref[n] = nref;
-        limit[n] = nref + (kOver - step_top);
+        // (less what large scores may be rounded by: 2 ulp of the reference)
+        limit[n] = nref + (kOver - step_top) - 0x1p-22f * fabsf(nref);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
 #pragma unroll
