@@ -356,6 +356,9 @@ wq_status wq_kv_read(const void* cache, void* k, void* v, int64_t ld_k, int64_t 
  * all groups: products below 2^-16 of it lose bits (its smallest steps are 2^-26
  * of it).  Value steps s are expected to be at least 2^-60 (smaller ones lose
  * bits).  The same call gives the same bits.
+ * All sequences of a call run in one form, chosen by their average number of
+ * rows: a long prompt beside many single tokens is faster as two calls (500 rows
+ * and 50 single ones, 32 heads, 4000 keys: 159 us in one, 63 + 36 in two).
  */
 size_t wq_kv_workspace_bytes(int rows, int batch, int ragged, int q_heads, int kv_heads, int head_dim,
                              int group, int max_kv_len);

@@ -146,7 +146,8 @@ struct KvPlan {
 };
 // Whether a wave may take two row tiles (they share every code it unpacks):
 // the sums of a tile take 16 registers per lane for every 64 channels, the
-// offsets 4 for every group, and 256 registers are to hold it all.
+// offsets 4 for every group.  256 registers hold that for every pair but 128
+// channels in groups of 64, which spills 12 to 15.
 constexpr bool kv_two_tiles(int head_dim, int group) { return head_dim <= 128 && head_dim / group <= 2; }
 // Waves per SIMD the registers of the one-tile key form leave room for.
 constexpr int kv_key_waves(int head_dim, int group) {
@@ -156,7 +157,10 @@ constexpr int kv_key_waves(int head_dim, int group) {
 inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv_heads, int head_dim,
                       int group, int64_t max_kv) {
   KvPlan p;
-  // packed rows (token, head) of a sequence, on average
+  // Packed rows (token, head) of a sequence, on average: the host does not know
+  // the offsets of a ragged batch.  A long chunk beside many single tokens then
+  // runs in a form that suits only one of them: 500 rows and 50 single ones of 32
+  // heads (8 of the cache) over 4000 keys take 159 us, 63 and 36 as two calls.
   const int64_t per = ((int64_t)rows * heads_per_kv + batch - 1) / batch;
   p.rows_form = per > 32;
   p.nq = per > 16 && kv_two_tiles(head_dim, group) ? 2 : 1;
@@ -190,9 +194,12 @@ inline KvPlan kv_plan(int rows, int batch, bool ragged, int heads_per_kv, int kv
   p.splits = s < 1 ? 1 : (int)s;
   p.nw = 4;
   // Short contexts of few rows take one workgroup of eight waves instead of
-  // parts and their join: over 1037 keys 10.3 us on the GPU against 10.0, and
-  // 10.7 against 14.7 for a call that is not captured (one launch, no
-  // workspace); over 2000 keys 13.1 against 10.2.
+  // parts and their join.  On the GPU, 32 heads of 128 / 64 heads of 64, in us
+  // against parts: 7.8 : 9.7 / 6.4 : 8.8 over 512 keys, 10.0 : 9.8 / 7.9 : 8.9
+  // over 1037, 10.1 : 9.8 / 8.1 : 8.8 over 1280, 11.1 : 9.8 / 8.9 : 8.9 over 1536,
+  // 12.8 : 9.9 / 10.1 : 8.9 over 2048.  A call that is not captured (one launch,
+  // no workspace) is bound by the host: 10.1 against 14.1 up to 1280, 12.6 against
+  // 14.0 over 2048.
   if (!p.rows_form && p.nq == 1 && p.splits > 1 && max_kv <= 1280) {
     p.nw = 8;
     p.splits = 1;

@@ -41,17 +41,25 @@
 // What bounds it (D = 128, one group, MI355X).  Decode: the bytes of the cache --
 // 48 rows of 8 heads over 2000 to 8000 keys, 260 MB, in 54-57 us, 4.6-4.8 TB/s
 // where a copy of 4 GiB reaches 4.9; about half of the vector instructions' time
-// fits beside it.  Many rows: vector instructions.  For a block of 64 keys and 32
-// rows a wave issues about 490 of them (160 unpack 32 words of codes, which two
-// row tiles share; about nine for each of a lane's 32 scores, one of them the
-// exponential at a quarter of the rate) beside 68 MFMAs of 16 cycles: 4096-row
-// prompts run in 345 us (797 TFLOP/s, vector units 81 % busy, matrix units 34 %).
+// fits beside it.  Many rows: vector instructions.  By the counters a wave issues
+// 618 for a block of 64 keys and 32 rows, its prologue, masked blocks and new
+// references shared out among them: 68 are MFMAs of 16 cycles, 160 unpack 32 words
+// of codes, which two row tiles share, and about nine go to each of a lane's 32
+// scores, one of them the exponential at a quarter of the rate.  4096-row prompts
+// run in 347 us (792 TFLOP/s, vector units 81 % busy, matrix units 34 %).
 // Measured and not kept: three and four row tiles per wave (their sums spill or
 // leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
 // against 137 on 1792 rows of 7 sequences), runs of blocks with and without hidden
 // keys in loops of their own (copies of the sums, spills: 2066 us), wave
 // priorities (-3 to +7 % by shape), the offsets' start of the scores from the
 // matrix cores (351 us).
+//
+// Registers: every form fits the 256 of two waves per SIMD but two row tiles of
+// D = 128 in groups of 64 (15 and 12 words spilled, rows and keys split) and D = 256
+// in groups of 32 (34-40; in groups of 64 one, rows split).  Those lie furthest from
+// the memory's and the matrix cores' rates: a 4096-row prompt of 32 heads of 128 in
+// groups of 128 / 64 / 32 takes 189 / 236 / 404 us, one of 16 heads of 256 takes
+// 215 / 270 / 480, and 32 rows of 16 heads of 256 over 4000 keys 49 / 52 / 138.
 //
 // Two forms.  Few rows per sequence (decode): the waves of a workgroup
 // take the blocks of 64 keys in turn and merge through LDS.  Many rows: each
@@ -353,7 +361,7 @@ void kv_attention_kernel(const KvAttnArgs a) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         // a copy for every tile: the broadcasts then stay operand modifiers (not
-        // where it would spill: D = 128 in two groups, 502 us against 475)
+        // where more would spill: D = 128 in two groups, 502 us against 475)
         float r = kr[g];
         if (NQ > 1 && (NG == 1 || D == 64)) asm volatile("" : "+v"(r));
         sfor<16>([&](auto ic) __attribute__((always_inline)) {

@@ -11,6 +11,9 @@ All of them name rows and sequences the same way:
                rows / batch rows each (one each in a decode step)
 
 so the rows of sequence b are its last cu_q[b + 1] - cu_q[b] positions.
+
+`stream` gives a call to another stream than the current one.  What it allocates comes from that stream's memory; that
+the cache and the tensors it is given are ready there is the caller's to see to.
 """
 from __future__ import annotations
 
