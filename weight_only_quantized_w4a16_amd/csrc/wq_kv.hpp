@@ -147,7 +147,7 @@ struct KvPlan {
 // Whether a wave may take two row tiles (they share every code it unpacks):
 // the sums of a tile take 16 registers per lane for every 64 channels, the
 // offsets 4 for every group.  256 registers hold that for every pair but 128
-// channels in groups of 64, which spills 12 to 15.
+// channels in groups of 64, which spills 11 to 13.
 constexpr bool kv_two_tiles(int head_dim, int group) { return head_dim <= 128 && head_dim / group <= 2; }
 // Waves per SIMD the registers of the one-tile key form leave room for.
 constexpr int kv_key_waves(int head_dim, int group) {

@@ -24,13 +24,13 @@
 // lies in [2^13, 2^14) and converted to fp16 (exact for fp16 and bf16 inputs
 // but for channels 2^-23 below the largest).  P = p s is rounded to fp16 once.
 // What it is relative to is the row's own: set so that the largest p s of the keys
-// it has seen lies at 2^6, and set anew once one may pass 2^15.5.  Every second
-// key's P carries a 2^-4 (its codes the 2^4), so products down to 2^-16 of the
-// row's largest are normal numbers, and half a step of the smallest is 2^-27 of
-// it.  Keys a row does not see, and keys that count for nothing however large
-// their values, have no part in that.  (The room upwards is what keeps the sums
-// from being scaled again and again: 2^10 to 2^14 took 366 us where 2^6 to 2^15.5
-// takes 348.)  The offsets are added as
+// it has seen lies at 2^6 (up to 2^7 with several groups), and set anew once one
+// may pass 2^15.5.  Every second key's P carries a 2^-4 (its codes the 2^4), so
+// products down to 2^-16 of the row's largest are normal numbers, and half a step
+// of the smallest is 2^-27 of it.  Keys a row does not see, and keys that count for
+// nothing however large their values, have no part in that.  (The room upwards is
+// what keeps the sums from being scaled again and again: a prompt with 2^10 to 2^14
+// took 366 us, 346 with 2^6 to 2^15.5.)  The offsets are added as
 // sum P lo / s beside sum P c, from the same rounded P, so that a rounding of P
 // shows times v / s rather than times c: lo / s, as the sum of two fp16, is one
 // more operand tile of the second product (rows 0 and 1 of it).  fp16 outputs,
@@ -46,7 +46,7 @@
 // references shared out among them: 68 are MFMAs of 16 cycles, 160 unpack 32 words
 // of codes, which two row tiles share, and about nine go to each of a lane's 32
 // scores, one of them the exponential at a quarter of the rate.  4096-row prompts
-// run in 347 us (792 TFLOP/s, vector units 81 % busy, matrix units 34 %).
+// run in 346 us (795 TFLOP/s, vector units 81 % busy, matrix units 34 %).
 // Measured and not kept: three and four row tiles per wave (their sums spill or
 // leave one wave per SIMD: 444 and 549 us), a wave of 48 rows with D = 64 (187 us
 // against 137 on 1792 rows of 7 sequences), runs of blocks with and without hidden
@@ -55,8 +55,8 @@
 // matrix cores (351 us).
 //
 // Registers: every form fits the 256 of two waves per SIMD but two row tiles of
-// D = 128 in groups of 64 (15 and 12 words spilled, rows and keys split) and D = 256
-// in groups of 32 (34-40; in groups of 64 one, rows split).  Those lie furthest from
+// D = 128 in groups of 64 (11 to 13 words spilled) and D = 256 in groups of 32 (36
+// to 39; in groups of 64 one, rows split).  Those lie furthest from
 // the memory's and the matrix cores' rates: a 4096-row prompt of 32 heads of 128 in
 // groups of 128 / 64 / 32 takes 189 / 236 / 404 us, one of 16 heads of 256 takes
 // 215 / 270 / 480, and 32 rows of 16 heads of 256 over 4000 keys 49 / 52 / 138.
@@ -76,7 +76,7 @@ namespace wq {
 namespace {
 
 constexpr float kNone = -1e30f;    // reference of a row that has seen no key
-constexpr float kTop = 6.0f;      // log2 of a row's largest p s when its reference is set
+constexpr float kTop = 6.0f;       // log2 of a row's largest p s when its reference is set, at least
 constexpr float kOver = 15.5f;     // log2 that p s may reach before it is set anew (fp16 ends at 16)
 constexpr float kStepMin = 0x1p-60f;    // references count smaller value steps as this
 constexpr float kStepZero = 0x1p-100f;  // smaller value steps (bf16 only) count as none
@@ -443,7 +443,7 @@ void kv_attention_kernel(const KvAttnArgs a) {
     if (__any(over)) {
       // The bound on the steps follows this block's, down too: a block of larger
       // ones costs itself and the next block this pass (half again as much room as
-      // this block needs: 348 us; the next power of two: 352).  New references where
+      // this block needs: a prompt in 348 us; the next power of two: 352).  New references where
       // a key the row sees calls for one (a hidden key's score is -inf): sums so far
       // are brought to them.
       int sx = __float_as_int(smax);  // positive: ordered as integers
@@ -460,7 +460,19 @@ void kv_attention_kernel(const KvAttnArgs a) {
         });
         t = fmaxf(t, __shfl_xor(t, 16, 64));
         t = fmaxf(t, __shfl_xor(t, 32, 64));
-        const float nref = fmaxf(ref[n], t - kTop);
+        // With several groups, a whole number of octaves from the largest score: the
+        // key that counts most then has P = s 2^e, which fp16 holds exactly in every
+        // group (with one group its P is 2^kTop).
+        float to = t - kTop;
+        if constexpr (NG > 1) {
+          float m = u[n][0][0];
+#pragma unroll
+          for (int i = 1; i < 16; ++i) m = fmaxf(m, u[n][i / 4][i % 4]);
+          m = fmaxf(m, __shfl_xor(m, 16, 64));
+          m = fmaxf(m, __shfl_xor(m, 32, 64)) * cq[n];
+          to = m + __builtin_floorf(to - m);
+        }
+        const float nref = fmaxf(ref[n], to);
         const float al = __builtin_amdgcn_exp2f(ref[n] - nref);
         sum[n] = scale_sum(sum[n], ref[n] - nref);
         ref[n] = nref;
