@@ -35,7 +35,7 @@
 // shows times v / s rather than times c: lo / s, as the sum of two fp16, is one
 // more operand tile of the second product (rows 0 and 1 of it).  fp16 outputs,
 // one row over 1037 keys: 0.39e-3 of the norm when the offsets were summed apart,
-// 0.22e-3 now; the rounding of the output alone is 0.20e-3.  A group without a step
+// 0.25e-3 now; the rounding of the output alone is 0.20e-3.  A group without a step
 // (all channels alike) takes |lo| for one.  Scores, maxima and sums are fp32.
 //
 // What bounds it (D = 128, one group, MI355X).  Decode: the bytes of the cache --
