@@ -134,6 +134,15 @@ def test_shared_rows_are_refused(L):
         assert rows_call(L, "wq_kv_read", k=base, v=v, ld_k=ld_k, ld_v=ld_v) == 1, (v, ld_k, ld_v)
 
 
+def test_workspace_of_lengths_past_32_bits(L):
+    """The size asked for is the size the call asks of its workspace, whatever length is expected."""
+    args = (1, 1, False, 8, 8, 128, 128)
+    most = wq.wq_kv_workspace_bytes(*args, 1 << 30)
+    assert most > wq.wq_kv_workspace_bytes(*args, 5000) > 0
+    for n in ((1 << 30) + 1, 1 << 31, (1 << 32) + 5000, 1 << 40):
+        assert wq.wq_kv_workspace_bytes(*args, n) == most, n
+
+
 @pytest.fixture(scope="module")
 def cache(L):
     return wq.wq_kv_cache(4, 16, 2, 64, 64, torch.float16, device="cpu")

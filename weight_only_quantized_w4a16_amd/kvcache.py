@@ -165,10 +165,10 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
 
 def wq_kv_workspace_bytes(rows: int, batch: int, ragged: bool, q_heads: int, kv_heads: int, head_dim: int,
                           group: int, max_kv_len: int) -> int:
-    """Scratch of a wq_kv_attention call with these sizes (ragged: with cu_q; max_kv_len: at most 2^30).
-    Fewer rows may need more of it: ask for every shape that is used."""
+    """Scratch of a wq_kv_attention call with these sizes (ragged: with cu_q; max_kv_len: past 2^30 as 2^30, as that
+    call takes it).  Fewer rows may need more of it: ask for every shape that is used."""
     return int(lib().wq_kv_workspace_bytes(rows, batch, int(bool(ragged)), q_heads, kv_heads, head_dim, group,
-                                           max_kv_len))
+                                           min(max_kv_len, 1 << 30)))
 
 
 def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
