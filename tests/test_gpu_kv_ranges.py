@@ -46,7 +46,8 @@ def reference(q, K, V, pos, scale, G, causal=True, window=0):
     Vmag = (vlo.abs()[..., None] + vs[..., None] * vc).flatten(2)
     flat = (vs == 0)[..., None]
     step = torch.where(vs > 0, vs, vlo.abs())
-    times = torch.where(flat, torch.ones_like(vc), vlo.abs()[..., None] / vs.clamp_min(1e-300)[..., None] + vc).flatten(2)
+    ratio = vlo.abs()[..., None] / vs.clamp_min(1e-300)[..., None]
+    times = torch.where(flat, torch.ones_like(vc), ratio + vc).flatten(2)
     steps = step[..., None].expand(-1, -1, -1, G).flatten(2)
     key = torch.arange(K.shape[0])
     bound = torch.zeros_like(out)
@@ -67,7 +68,8 @@ def reference(q, K, V, pos, scale, G, causal=True, window=0):
             largest = float((w * step[seen, kh].amax(1)).max())
             b = (w @ Vmag[seen, kh]) * (2.0 ** -11 + 2 * ep + (int(seen.sum()) + 16) * 2.0 ** -24)
             b += 2.0 ** -27 * largest * times[seen, kh].sum(0) + 2.0 ** -21 * (w @ steps[seen, kh])
-            bound[i, h] = b + _kv.EPS[q.dtype] / 2 * (out[i, h].abs() + b) + torch.finfo(q.dtype).tiny * _kv.EPS[q.dtype] / 2
+            half = _kv.EPS[q.dtype] / 2
+            bound[i, h] = b + half * (out[i, h].abs() + b) + half * torch.finfo(q.dtype).tiny
     return out, bound
 
 
@@ -90,7 +92,8 @@ HIDDEN = [(F16, 2.0 ** -9, 2.0 ** 18), (F16, 2.0 ** -9, 2.0 ** 21), (BF16, 1.0, 
 
 
 @pytest.mark.parametrize("dt,base,factor", HIDDEN)
-@pytest.mark.parametrize("D,G,heads,new", [(64, 64, 2, 64), (64, 64, 1, 12), (128, 64, 4, 40), (128, 128, 4, 5), (256, 64, 2, 30)])
+@pytest.mark.parametrize("D,G,heads,new", [(64, 64, 2, 64), (64, 64, 1, 12), (128, 64, 4, 40), (128, 128, 4, 5),
+                                           (256, 64, 2, 30)])
 def test_larger_values_of_later_tokens(wq, dt, base, factor, D, G, heads, new):
     """The last tokens of a prompt hold far larger values: the rows before them do not change."""
     P = _kv.Problem([64 + 5], [new], 1, D, G, 16, dt, D + new, scale=1.0)
@@ -212,7 +215,8 @@ def test_unwritten_pages_before_the_window(wq, dt, new):
     P = _kv.Problem([n], [new], 1, 64, 64, 16, dt, 60 + new)
     q = P.queries(2)
     want, bound = reference(q, P.K[0], P.V[0], torch.arange(n - new, n), 0.125, 64, window=window)
-    for s, lo in ((inf, inf), (inf, 0), (1, big), (1, big | 0x8000), (0x3C00, inf), (0x8001, inf | 0x8000), (0xFFFF, 0xFFFF)):
+    for s, lo in ((inf, inf), (inf, 0), (1, big), (1, big | 0x8000), (0x3C00, inf), (0x8001, inf | 0x8000),
+                  (0xFFFF, 0xFFFF)):
         cache = P.empty(wq)
         P.fill(wq, cache)
         word = (s | lo << 16)

@@ -147,3 +147,38 @@ def test_products_on_another_stream_beside_pending_work(busy):
     torch.cuda.synchronize()
     assert torch.equal(kept, want1) and torch.equal(got, want2)
     assert torch.equal(w, wq.wq_dequant_debug(layer, torch.float16))
+
+
+@pytest.mark.gpu
+def test_a_captured_branch_on_another_stream():
+    """A graph whose capture forks to a second stream: outputs and scratch of the calls on it come from the graph's own
+    memory, and every replay gives the eager results."""
+    P = _kv.Problem([3000], [1], 2, 128, 128, 16, torch.float16, 3)
+    cache = P.empty(wq)
+    P.fill(wq, cache)
+    args = (cache, P.table.cuda(), i32([3000]))
+    q = torch.randn(1, 8, 128).half().cuda()
+    x = torch.randn(64, 512).half().cuda()
+    assert wq.wq_kv_workspace_bytes(1, 1, False, 8, 2, 128, 128, args[1].shape[1] * 16) > 0
+    for _ in range(2):
+        wq.wq_kv_attention(q, *args), wq.wq_hadamard(x, 64)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        a = wq.wq_kv_attention(q, *args, stream=side)
+        k, v = wq.wq_kv_read(*args, 1, stream=side)
+        b = wq.wq_kv_attention(q, *args)
+        r = wq.wq_hadamard(x, 64, stream=side)
+        main.wait_stream(side)
+    for i in range(4):
+        q.copy_(torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(i)))
+        x.mul_(0.5)
+        want = wq.wq_kv_attention(q, *args)
+        want_k, want_v = wq.wq_kv_read(*args, 1)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want) and torch.equal(r, wq.wq_hadamard(x, 64)), i
+        assert torch.equal(k, want_k) and torch.equal(v, want_v), i
