@@ -9,7 +9,7 @@ import weight_only_quantized_w4a16_amd as wq
 
 
 def test_memory_is_allocated_on_the_launching_stream(monkeypatch):
-    """(CPU) With another stream given, torch.empty runs under it; what is returned is recorded on the current one."""
+    """(CPU) With another stream given, memory is allocated under it; what is returned is recorded on the current one."""
     seen = []
 
     class Stream:
@@ -31,24 +31,25 @@ def test_memory_is_allocated_on_the_launching_stream(monkeypatch):
         yield
         active.pop()
 
-    def empty(shape, dtype, device):
-        seen.append((shape, dtype, device))
-        return Tensor()
+    class Like:
+        device = torch.device("cuda", 0)
+
+        def new_empty(self, shape, dtype):
+            seen.append((shape, dtype))
+            return Tensor()
 
     side, current = Stream(7), Stream(3)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: current.cuda_stream, raising=False)
     monkeypatch.setattr(torch.cuda, "stream", under)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: current)
-    monkeypatch.setattr(torch, "empty", empty)
-    dev = torch.device("cuda", 0)
     for stream in (None, current):
-        t = wq._empty(stream, (2, 3), torch.float16, dev)
+        t = wq._empty(stream, Like(), (2, 3))
         assert t.made_on == [] and t.recorded == []
-    t = wq._empty(side, (2, 3), torch.float16, dev)
+    t = wq._empty(side, Like(), (2, 3))
     assert t.made_on == [side] and t.recorded == [current]
-    t = wq._empty(side, 64, torch.uint8, dev, scratch=True)
+    t = wq._empty(side, Like(), 64, torch.uint8, scratch=True)
     assert t.made_on == [side] and t.recorded == []
-    assert len(seen) == 4 and active == []
+    assert seen == [((2, 3), None)] * 3 + [(64, torch.uint8)] and active == []
 
 
 @pytest.fixture()

@@ -104,16 +104,17 @@ def _stream(stream, dev: torch.device) -> int:
     return stream.cuda_stream
 
 
-def _empty(stream, shape, dtype: torch.dtype, dev: torch.device, scratch: bool = False) -> torch.Tensor:
-    """Memory for work on `stream` (the current one by default).  It comes from that stream's own: memory of the
+def _empty(stream, like: torch.Tensor, shape, dtype: Optional[torch.dtype] = None,
+           scratch: bool = False) -> torch.Tensor:
+    """Memory on the device (and, by default, of the type) of `like` for work on `stream` (None: the current one).  It comes from that stream's own: memory of the
     current stream may still be in use there by work its last owner left behind, which another stream does not wait
     for.  What the caller gets (not scratch) is also kept for what the current stream does with it."""
     if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(stream.device_index):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = like.new_empty(shape, dtype=dtype)
     if not scratch:
-        t.record_stream(torch.cuda.current_stream(dev))
+        t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
@@ -218,13 +219,13 @@ def _repack(fn: str, qweight, scales, zeros, mode, g_idx, K, N, bits, group_size
     if nbytes == 0:
         raise WQError("wq_packed_bytes", 2)
     at = _stream(stream, dev)
-    packed = _empty(stream, nbytes, torch.uint8, dev)
+    packed = _empty(stream, qweight, nbytes, torch.uint8)
     perm = None
     g_host = None
     if g_idx is not None:
         import numpy as np
         g_host = np.ascontiguousarray(torch.as_tensor(g_idx).cpu().numpy(), dtype=np.int32)
-        perm = _empty(stream, K, torch.int32, dev)
+        perm = _empty(stream, qweight, K)
     rc = getattr(lib(), fn)(_ptr(qweight), _ptr(scales), _ptr(zeros), mode,
                             None if g_host is None else ctypes.c_void_p(g_host.ctypes.data),
                             K, N, bits, group_size, _ptr(packed), _ptr(perm), at)
@@ -274,7 +275,7 @@ def wq_dequant_debug(layer: PackedLayer, dtype: torch.dtype, stream=None) -> tor
     _check_layer(layer, layer.packed.device)
     _check_cuda(layer.packed, "layer.packed")
     at = _stream(stream, layer.packed.device)
-    w = _empty(stream, (layer.K, layer.N), dtype, layer.packed.device)
+    w = _empty(stream, layer.packed, (layer.K, layer.N), dtype)
     rc = lib().wq_dequant_debug(_ptr(layer.packed), layer.mode, _ptr(layer.lut), _ptr(layer.perm),
                                 layer.K, layer.N, layer.bits, layer.group_size, _dt(dtype), _ptr(w), at)
     _check("wq_dequant_debug", rc)
@@ -320,9 +321,9 @@ def _product(fn: str, x: torch.Tensor, layer: PackedLayer, out: Optional[torch.T
     _check_cuda(x, "x")
     at = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, (M, ncols), x.dtype, dev)
+        out = _empty(stream, x, (M, ncols))
     if need and ws is None:
-        ws = _empty(stream, need, torch.uint8, dev, scratch=True)
+        ws = _empty(stream, x, need, torch.uint8, scratch=True)
     rc = getattr(L, fn)(x.data_ptr(), dt, layer.packed.data_ptr(), layer.mode, _ptr(layer.lut), _ptr(layer.perm),
                         *extra, out.data_ptr(), M, layer.N, layer.K, layer.bits, layer.group_size,
                         ws.data_ptr() if need else None, need, at)
@@ -398,7 +399,7 @@ def wq_hadamard(x: torch.Tensor, block: int, out: Optional[torch.Tensor] = None,
     _check_cuda(x, "x")
     at = _stream(stream, x.device)
     if out is None:
-        out = _empty(stream, (M, K), x.dtype, x.device)
+        out = torch.empty_like(x) if stream is None else _empty(stream, x, (M, K))
     rc = lib().wq_hadamard(_ptr(x), _dt(x.dtype), _ptr(out), M, K, block, at)
     _check("wq_hadamard", rc)
     return out

@@ -58,6 +58,7 @@ bool rows_meet(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int row
   typedef __int128 Z;  // (any stride)
   if (rows == 1) ld_a = ld_b = width;
   const Z d = ((Z)(uintptr_t)b - (Z)(uintptr_t)a) / 2;  // both are 16-byte aligned
+  if (d >= (rows - 1) * (Z)ld_a + width || -d >= (rows - 1) * (Z)ld_b + width) return false;
   // rows of a from the first that ends behind b's beginning on; for each the
   // first row of b that ends behind its beginning
   for (Z i = d < width ? 0 : (d - width) / ld_a + 1; i < rows; ++i) {

@@ -152,7 +152,7 @@ def wq_kv_read(cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
     _check_cuda(data, "cache.data")
     at = _stream(stream, dev)
     if out is None:
-        k, v = (_empty(stream, (rows, cache.kv_heads, cache.head_dim), cache.dtype, dev) for _ in range(2))
+        k, v = (_empty(stream, data, (rows, cache.kv_heads, cache.head_dim), cache.dtype) for _ in range(2))
         k_at, v_at, ld_k = k.data_ptr(), v.data_ptr(), cache.kv_heads * cache.head_dim
         ld_v = ld_k
     rc = lib().wq_kv_read(data.data_ptr(), k_at, v_at, ld_k, ld_v, cache.dt, block_table.data_ptr(),
@@ -214,10 +214,10 @@ def wq_kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     _check_cuda(data, "cache.data")
     at = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, (rows, q_heads, cache.head_dim), cache.dtype, dev)
+        out = _empty(stream, q, (rows, q_heads, cache.head_dim))
         o_at, ld_o = out.data_ptr(), q_heads * cache.head_dim
     if need and ws is None:
-        ws = _empty(stream, need, torch.uint8, dev, scratch=True)
+        ws = _empty(stream, data, need, scratch=True)
     rc = L.wq_kv_attention(q_at, ld_q, cache.dt, data.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
                            _ptr(cu_q), o_at, ld_o, rows, batch, max_pages, cache.num_pages, cache.page_size, q_heads,
                            cache.kv_heads, cache.head_dim, cache.group, scale, 1 if causal else 0, window, max_kv_len,

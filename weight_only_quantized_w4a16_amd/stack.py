@@ -162,7 +162,7 @@ class CachedStack:
         need = wq_kv_workspace_bytes(T, batch, ragged, H, KV, D, self.caches[0].group,
                                      block_table.shape[1] * self.caches[0].page_size if max_kv_len is None
                                      else max_kv_len)
-        ws = _empty(stream, need, torch.uint8, x.device, scratch=True) if need else None
+        ws = _empty(stream, x, need, torch.uint8, scratch=True) if need else None
         cur = x
         for i, (L, cache) in enumerate(zip(self.layers, self.caches)):
             if record is not None:  # (the layer's output may be written over its input)
