@@ -53,7 +53,7 @@ METRIC = "weight GB/s (GEMV, M=1) & TFLOP/s (GEMM, M=2048) as % of HBM/MFMA roof
 KERNEL_SOURCES = ["wq_gemv.hip", "wq_decode.hpp", "wq_layout.hpp"]  # the dominant (GEMV) kernel's sources
 ALL_SOURCES = ["wq_api.hip", "wq_common.hpp", "wq_decode.hpp", "wq_gemm.hip", "wq_gemv.hip", "wq_hadamard.hip",
                "wq_layout.hpp"]
-KV_SOURCES = ["wq_kv.hpp", "wq_kv_api.hip", "wq_kv_attention.hip", "wq_kv_rows.hip"]
+KV_SOURCES = ["wq_kv.hpp", "wq_kv_api.hip", "wq_kv_attention.hip", "wq_kv_rows.hip"]  # cache operators'
 
 
 def parse():

@@ -230,7 +230,8 @@ def main():
     print("Summary command (repository root):\n\n    python prof_summary.py " + shlex.join(own) + "\n")
     sys.path.insert(0, ROOT)
     import bench
-    print(f"Kernel sources sha256/16: GEMV {bench.kernel_hash()}, all {bench.kernel_hash(bench.ALL_SOURCES)}\n")
+    print(f"Kernel sources sha256/16: GEMV {bench.kernel_hash()}, products {bench.kernel_hash(bench.ALL_SOURCES)}, "
+          f"cache {bench.kernel_hash(bench.KV_SOURCES)}\n")
     (trace if args.kind == "trace" else pmc)(args)
 
 
