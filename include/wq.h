@@ -368,6 +368,123 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
                           int group, float scale, int causal, int window, int max_kv_len, void* ws, size_t ws_bytes,
                           void* stream);
 
+/*
+ * ---- The rest of a decoder layer -------------------------------------------
+ * Norms, rotary positions, low-rank adapters and the cache's page tables, so
+ * that a step of a model runs from token lengths to its last layer's rows
+ * without the host.  Sequences, cu_q and kv_lens as above.
+ */
+
+/*
+ * wq_rms_norm -- root-mean-square norm of rows, with the residual's addition:
+ *     h = x + residual,  sum = h,  y = weight h / sqrt(mean(h^2) + eps)
+ * in fp32; y comes from the unrounded h, and y and sum are rounded to `dt` once.
+ *   x, residual, y, sum : [rows][heads][dim] in `dt`, each row's heads contiguous
+ *              and `ld_*` elements between rows (a multiple of 8; 16-byte aligned
+ *              base); every head is normalised by itself, heads = 1 for whole rows
+ *   residual : may be NULL (then sum too); sum may be NULL with a residual
+ *   weight   : [dim] in `dt`, 16-byte aligned
+ *   eps      : a positive normal fp32 number
+ * y or sum may be x or residual themselves (with their stride); other shared
+ * elements are WQ_EINVAL.  dim % 8 == 0, 8 <= dim <= 65536, heads <= 4096,
+ * rows <= 2^24, rows heads <= 2^28, rows heads dim <= 2^33 (else WQ_EUNSUPPORTED).  The sum of squares must
+ * stay within fp32: past it finite elements give 0, as in that arithmetic.
+ */
+wq_status wq_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
+                      float eps, wq_dtype dt, void* y, int64_t ld_y, void* sum, int64_t ld_sum, int rows, int heads,
+                      int dim, void* stream);
+
+/*
+ * wq_rotary -- rotary positions of one or several axes (time, height, width):
+ * pair i of every head of q and k turns by the angle
+ *     p[axis[i]] turns[i] / 2^64  of a whole turn,
+ * p the row's position on that axis, and is multiplied by `factor`.
+ *   q, k, q_out, k_out : [rows][heads][head_dim] in `dt`, strides as for the cache's
+ *              rows.  k and k_out may be NULL (kv_heads 0).  An output may be its
+ *              input itself (with its stride); other shared elements with an input
+ *              or the other output are WQ_EINVAL
+ *   turns    : device [rotary_dim / 2], the fraction of a turn per position in units
+ *              of 2^-64: the product with a position wraps where the angle does, so
+ *              far positions lose nothing
+ *   axis     : device int32 [rotary_dim / 2], each held to 0 .. axes - 1, or NULL (all 0)
+ *   adjacent : 0: pair i is channels (i, i + rotary_dim / 2), 1: (2 i, 2 i + 1);
+ *              channels from rotary_dim on are copied
+ *   positions: device int32 [axes][rows], `ld_positions` elements between axes (0: one
+ *              row for all axes), for every row; kv_lens and cu_q are not read then.
+ *              NULL: positions of sequences, the same on every axis, and rows outside
+ *              every sequence are left as they were
+ * head_dim % 8 == 0 and <= 512; rotary_dim <= head_dim, a multiple of 16 (of 8 with
+ * adjacent pairs); axes <= 16; heads <= 4096 (else WQ_EUNSUPPORTED).  Angles are
+ * exact to 2^-28 of a turn; fp32 arithmetic, outputs rounded to `dt` once.
+ */
+wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq_dtype dt, const uint64_t* turns,
+                    const int32_t* axis, float factor, const int32_t* positions, int64_t ld_positions,
+                    const int32_t* kv_lens, const int32_t* cu_q, void* q_out, int64_t ld_q_out, void* k_out,
+                    int64_t ld_k_out, int rows, int batch, int q_heads, int kv_heads, int head_dim, int rotary_dim,
+                    int adjacent, int axes, void* stream);
+
+/*
+ * wq_lora -- low-rank adapters of many sequences beside one shared projection:
+ *     out[t] = y[t] + scales[a] (x[t] A[a]^T) B[a]^T,  a = adapters[sequence of t],
+ * the columns in `slices` slices (fused QKV: three), slice s with its own rows
+ * A[a][s]; only the first ranks[a] rows of A[a][s] and columns of B[a] count.
+ *   x        : [rows][K] in `dt`;  y, out: [rows][N] in `dt`; out may be y itself,
+ *              other shared elements are WQ_EINVAL
+ *   a, b     : device [num_adapters][slices][rank][K] and [num_adapters][N][rank] in `dt`
+ *   scales   : device fp32 [num_adapters]
+ *   ranks    : device int32 [num_adapters], each held to 0 .. rank, or NULL (all `rank`).
+ *              What lies past an adapter's rank is not used, whatever it holds
+ *   slice_ends : host int32 [slices], ascending columns each slice ends at, multiples of
+ *              16, the last one N; slices <= 4
+ *   adapters : device int32 [batch]; a sequence whose number is not in 0 ..
+ *              num_adapters - 1 has none: its rows are y
+ *   ws       : wq_lora_workspace_bytes() bytes for these sizes, 16-byte aligned; calls
+ *              that overlap in time must not share it
+ * All pointers but adapters, scales, ranks and cu_q are 16-byte aligned.  K % 128 == 0,
+ * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24 (else
+ * WQ_EUNSUPPORTED).
+ * Rows outside every sequence are left as they were.  fp32 accumulation; x A^T enters
+ * the second product in two parts that hold it to 2^-16 (bf16) or 2^-22 (fp16) of the
+ * row's largest; out is rounded to `dt` once.  The same call gives the same bits.
+ */
+size_t wq_lora_workspace_bytes(int rows, int batch, int K, int rank, int slices);
+wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, const float* scales, const int32_t* ranks,
+                  const int32_t* adapters, const int32_t* cu_q, const void* y, void* out, int rows, int batch,
+                  int num_adapters, int N, int K, int rank, int slices, const int32_t* slice_ends_host, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/*
+ * wq_kv_resize -- sequences of the paged cache from kv_lens to want_lens tokens each:
+ * lengths, block table and the stack of free pages are changed in place, on the GPU.
+ * A sequence of n tokens holds the first ceil(n / page_size) entries of its row of the
+ * table; growing takes pages (prompts, new tokens), shrinking gives them back (guessed
+ * tokens that did not hold; 0: the sequence has ended) and leaves -1.  In the order
+ * (sequence, entry), the f-th page taken is the f-th given back, and past those
+ * free_pages[count + back - 1 - f]; the f-th given back, past the taken ones, goes to
+ * that place.  So shrinking what has just grown restores everything.  A page belongs to
+ * one sequence.
+ *   block_table, kv_lens : as above, read and written; lengths read are held to the table
+ *   want_lens  : device int32 [batch]
+ *   free_pages : device int32 [num_pages]; counts: device int32 [2], the first the number
+ *                of free pages
+ * All or nothing: where the free pages do not suffice, or a wanted length is below 0 or
+ * past the table, or more pages come back than there are, nothing is changed; counts[1]
+ * is 0, the number of pages lacking, or -1.  kv_lens, want_lens, block_table, free_pages
+ * and counts share no memory with each other or with an output (WQ_EINVAL).
+ * Outputs (each may be NULL), for the step that fills the new tokens:
+ *   cu_q      : int32 [batch + 1], offsets of the new rows (as every call takes them);
+ *               all 0 where nothing was changed
+ *   positions : int32 [rows], position of each new row
+ *   slots     : int64 [rows], its page * page_size + position % page_size
+ *               Rows past the new ones are -1; new rows past `rows` are not written.
+ *   ws        : wq_kv_resize_workspace_bytes() bytes, 16-byte aligned (NULL when 0)
+ * page_size as for the cache; batch <= 2^16, rows <= 2^24, max_pages page_size <= 2^30.
+ */
+size_t wq_kv_resize_workspace_bytes(int batch, int max_pages, int num_pages, int rows);
+wq_status wq_kv_resize(int32_t* block_table, int32_t* kv_lens, const int32_t* want_lens, int32_t* free_pages,
+                       int32_t* counts, int32_t* cu_q, int32_t* positions, int64_t* slots, int rows, int batch,
+                       int max_pages, int num_pages, int page_size, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

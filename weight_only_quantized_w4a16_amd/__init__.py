@@ -78,6 +78,18 @@ def lib() -> ctypes.CDLL:
         L.wq_kv_workspace_bytes.restype = Z
         L.wq_kv_attention.argtypes = [P, L64, I, P, P, P, P, P, L64] + [I] * 9 + [F, I, I, I, P, Z, P]
         L.wq_kv_attention.restype = I
+        L.wq_rms_norm.argtypes = [P, L64, P, L64, P, F, I, P, L64, P, L64, I, I, I, P]
+        L.wq_rms_norm.restype = I
+        L.wq_rotary.argtypes = [P, L64, P, L64, I, P, P, F, P, L64, P, P, P, L64, P, L64] + [I] * 8 + [P]
+        L.wq_rotary.restype = I
+        L.wq_lora_workspace_bytes.argtypes = [I] * 5
+        L.wq_lora_workspace_bytes.restype = Z
+        L.wq_lora.argtypes = [P, I] + [P] * 8 + [I] * 7 + [P, P, Z, P]
+        L.wq_lora.restype = I
+        L.wq_kv_resize_workspace_bytes.argtypes = [I] * 4
+        L.wq_kv_resize_workspace_bytes.restype = Z
+        L.wq_kv_resize.argtypes = [P] * 8 + [I] * 5 + [P, Z, P]
+        L.wq_kv_resize.restype = I
         if L.wq_layout_version() != LAYOUT_VERSION:
             raise RuntimeError("libwq.so layout version does not match this binding")
         _lib = L
@@ -441,3 +453,6 @@ def linear(x: torch.Tensor, layer: PackedLayer, out=None, ws=None, stream=None, 
 
 from .kvcache import (KVCache, wq_kv_attention, wq_kv_cache, wq_kv_cache_bytes, wq_kv_read,  # noqa: E402
                       wq_kv_workspace_bytes, wq_kv_write)
+from .lora import LoraBank, wq_lora, wq_lora_workspace_bytes  # noqa: E402
+from .pages import KVPages, wq_kv_pages, wq_kv_resize, wq_kv_resize_workspace_bytes  # noqa: E402
+from .rows import Rotary, wq_rms_norm, wq_rotary, wq_rotary_plan  # noqa: E402

@@ -13,7 +13,9 @@ PROBE_LIB = os.path.join(HERE, "libwq_probe.so")
 # (source, object name, extra defines): the kernel files are compiled once
 # per (activation dtype, code width) so the instantiations build in parallel.
 SOURCES = [("wq_api.hip", "wq_api", []), ("wq_hadamard.hip", "wq_hadamard", []), ("wq_kv_api.hip", "wq_kv_api", []),
-           ("wq_kv_rows.hip", "wq_kv_rows", [])]
+           ("wq_kv_rows.hip", "wq_kv_rows", []), ("wq_kv_pages.hip", "wq_kv_pages", []),
+           ("wq_layer_api.hip", "wq_layer_api", []), ("wq_norm.hip", "wq_norm", []),
+           ("wq_rotary.hip", "wq_rotary", []), ("wq_lora.hip", "wq_lora", [])]
 # the cache attention once per head size
 for _d in (256, 192, 128, 96, 64):
     SOURCES.append(("wq_kv_attention.hip", f"wq_kv_attention_{_d}", [f"-DWQ_HEAD_DIM={_d}"]))

@@ -4,13 +4,12 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "wq_checks.hpp"
 #include "wq_kv.hpp"
 
 using namespace wq;
 
 namespace {
-
-bool power_of_two(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
 // The shape of a cache: every page of every kv head.
 wq_status check_cache(int num_pages, int page_size, int kv_heads, int head_dim, int group) {
@@ -44,33 +43,6 @@ wq_status make_seqs(KvSeqs& s, const int32_t* block_table, const int32_t* kv_len
   return WQ_OK;
 }
 
-// Row matrices [rows][heads * head_dim] with a row stride: 16-byte loads.
-wq_status check_rows(const void* p, int64_t ld, int rows, int width) {
-  if (!p) return WQ_EINVAL;
-  if (rows > 1 && ld < width) return WQ_EINVAL;
-  if (((uintptr_t)p & 15) || (rows > 1 && ld % 8 != 0)) return WQ_EUNSUPPORTED;
-  return WQ_OK;
-}
-
-// Whether two matrices of `rows` rows of `width` elements share one.  The rows of
-// one may lie between those of the other (slices of one buffer).
-bool rows_meet(const void* a, int64_t ld_a, const void* b, int64_t ld_b, int rows, int width) {
-  typedef __int128 Z;  // (any stride)
-  if (rows == 1) ld_a = ld_b = width;
-  const Z d = ((Z)(uintptr_t)b - (Z)(uintptr_t)a) / 2;  // both are 16-byte aligned
-  if (d >= (rows - 1) * (Z)ld_a + width || -d >= (rows - 1) * (Z)ld_b + width) return false;
-  // rows of a from the first that ends behind b's beginning on; for each the
-  // first row of b that ends behind its beginning
-  for (Z i = d < width ? 0 : (d - width) / ld_a + 1; i < rows; ++i) {
-    const Z at = i * ld_a - d;  // from b's beginning
-    const Z j = at < width ? 0 : (at - width) / ld_b + 1;
-    if (j >= rows) return false;
-    if (j * ld_b < at + width) return true;
-    if (ld_a == ld_b && at >= width) return false;  // the same for every further row
-  }
-  return false;
-}
-
 wq_status kv_rows(bool write, void* cache, const void* k, const void* v, int64_t ld_k, int64_t ld_v, wq_dtype dt,
                   const int32_t* block_table, const int32_t* kv_lens, const int32_t* cu_q, int rows, int batch,
                   int max_pages, int num_pages, int page_size, int kv_heads, int head_dim, int group, void* stream) {
@@ -85,7 +57,7 @@ wq_status kv_rows(bool write, void* cache, const void* k, const void* v, int64_t
   if ((uintptr_t)cache & 127) return WQ_EUNSUPPORTED;
   if ((st = check_rows(k, ld_k, rows, kv_heads * head_dim)) != WQ_OK) return st;
   if ((st = check_rows(v, ld_v, rows, kv_heads * head_dim)) != WQ_OK) return st;
-  if (!write && rows_meet(k, ld_k, v, ld_v, rows, kv_heads * head_dim)) return WQ_EINVAL;
+  if (!write && rows_meet(k, ld_k, kv_heads * head_dim, v, ld_v, kv_heads * head_dim, rows)) return WQ_EINVAL;
   // grid: four records of one head, keys or values, to a workgroup
   if (((int64_t)rows / 16 + 2 * (int64_t)batch) * kv_heads * 2 >= ((int64_t)1 << 31)) return WQ_EUNSUPPORTED;
   return launch_kv_rows(write, s, (uint8_t*)cache, (uint16_t*)const_cast<void*>(k),
@@ -163,7 +135,7 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
   if ((int64_t)p.slots * p.splits * kv_heads >= ((int64_t)1 << 23) || (int64_t)rows * q_heads > ((int64_t)1 << 30))
     return WQ_EUNSUPPORTED;
   // in place, or apart: other rows of q would be overwritten before they are read
-  if (!(q == out && (rows == 1 || ld_q == ld_out)) && rows_meet(q, ld_q, out, ld_out, rows, q_heads * head_dim))
+  if (!(q == out && (rows == 1 || ld_q == ld_out)) && rows_meet(q, ld_q, q_heads * head_dim, out, ld_out, q_heads * head_dim, rows))
     return WQ_EINVAL;
   const size_t part = kv_part_bytes(p, rows, q_heads, head_dim), need = part + kv_ml_bytes(p, rows, q_heads);
   if (need && (!ws || ws_bytes < need)) return WQ_ENOSPACE;
