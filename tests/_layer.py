@@ -59,20 +59,23 @@ def lora(x, y, a, b, scales, ranks, slices, ids):
     r = a.shape[-2]
     out, err = y.double(), torch.zeros(y.shape, dtype=torch.float64)
     u, parts = 2.0 ** -24, 2.0 ** -16 if dt == torch.bfloat16 else 2.0 ** -22
-    for t in range(T):
-        i = ids[t]
+    ids_t = torch.tensor(ids)
+    for i in sorted(set(ids)):
         if i < 0 or i >= a.shape[0]:
             continue
-        k, at = ranks[i], 0
+        rows = (ids_t == i).nonzero().flatten()
+        X, k, at, w = x[rows].double(), ranks[i], 0, abs(float(scales[i]))
         for s, n in enumerate(slices):
-            A, B = a[i, s, :k].double(), b[i, at:at + n, :k].double()
-            v, mag = A @ x[t].double(), A.abs() @ x[t].double().abs()
-            ev = mag * (32 + K / 32 + 64) * u + parts * (v.abs().max() if k else 0.0)
-            w = abs(float(scales[i]))
-            out[t, at:at + n] += float(scales[i]) * (B @ v)
-            err[t, at:at + n] = w * (B.abs() @ (ev + (2 * r + 8) * u * v.abs())) * (1 + 2.0 ** -10)
+            A, B = a[i, s, :k].double().t().contiguous(), b[i, at:at + n, :k].double().t().contiguous()
+            v, mag = X @ A, X.abs() @ A.abs()
+            ev = mag * (32 + K / 32 + 64) * u
+            if k:
+                ev = ev + parts * v.abs().amax(1, keepdim=True)
+            delta = float(scales[i]) * (v @ B)
+            out[rows, at:at + n] += delta
+            err[rows, at:at + n] = (w * ((ev + (2 * r + 8) * u * v.abs()) @ B.abs()) * (1 + 2.0 ** -10)
+                                    + (out[rows, at:at + n].abs() + delta.abs()) * 2.0 ** -22)
             at += n
-        err[t] += (out[t].abs() + (out[t] - y[t].double()).abs()) * 2.0 ** -22
     none = torch.tensor([not 0 <= i < a.shape[0] for i in ids])[:, None]
     return out, torch.where(none, torch.zeros_like(err), err + rounding(out, dt))
 

@@ -44,7 +44,9 @@ struct LoraArgs {
   const int32_t* adapters;
   const uint16_t* y;
   uint16_t* out;
-  float* part;           // x A^T: [rows][slices * rank]
+  float* part;           // workspace: parts of x A^T, [parts][rows][slices * rank]; launch_lora sets the next two
+  uint16_t* v;
+  float* down;
   KvSeqs seqs;           // cu_q, rows, batch
   int num, N, K, rank, slices;
   int ends[kLoraMaxSlices];

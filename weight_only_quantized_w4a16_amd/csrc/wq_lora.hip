@@ -2,20 +2,24 @@
 //
 // out = y + scale (x A^T) B^T, each row with its sequence's adapter, in two
 // products on the matrix cores: v = x A^T in fp32 parts of the K axis, then
-// v B^T added to y.  Rows are taken in tiles of 16 or 64 whatever sequences they
-// belong to; a tile works through the distinct adapters among its rows, each
-// read once for all of that adapter's rows, the columns of other rows left out
-// of loads and stores.  Where rows are few (decode steps: a tile may hold 16
-// adapters) the distinct adapters of a tile are spread over workgroups.
+// v B^T added to y.  Rows are taken in tiles of 64 whatever sequences they belong
+// to; a tile works through the distinct adapters among its rows, each read once
+// for all of that adapter's rows in the tile, other rows left out of loads and
+// stores.  Where rows are few the tile's work items -- an adapter and up to four
+// (first product) or 16 (second) of its rows -- are spread over workgroups.
 //
-// In the first product the rows of A are the MFMA's first operand, so a lane
-// ends with four consecutive entries of one row's v; the waves of a workgroup
-// split K and add up through LDS.  In the second the rows of B are, two tiles of
-// 16 columns dealt out so that a lane ends with eight consecutive columns of one
-// row: y is read and out written 16 bytes at a time.  v is fp32 and enters that
-// product as a sum of two 16-bit numbers (with one, its rounding alone would show
-// as much as the output's own); for fp16 each row's v is first scaled by a power
-// of two into the upper range of the type, exactly, and back behind the product.
+// v is fp32 and enters the second product as a sum of two 16-bit numbers: with
+// one, its rounding alone would show as much as the output's own.  For fp16 each
+// row's v is first scaled by a power of two into the upper range of the type,
+// exactly, and back behind the product.
+//
+// What bounds them (MI355X, graph-replayed, banks and rows from memory).  Few rows:
+// launches and the chain offsets -> adapter -> rank -> data; one row of rank 16
+// over 4096 x 4096 takes 7.6 us for 0.3 MB, 64 tokens of 40 adapters of ranks 8
+// to 32 beside 8192 -> 10240 20.5 us for 52 MB (first product 10.8 us at 3.3
+// TB/s, second 9.2).  Many: 6400 prompt rows of rank 64 beside 4096 -> 12288 take
+// 117 us: 34 us for x A^T (LDS and the latency of its stages), 6 to put its parts
+// together, 76 us for the 315 MB of y and out (4.1 TB/s; a copy: 4.75).
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -23,37 +27,56 @@ namespace {
 
 // Shape of a call, a function of the sizes the host knows.
 struct LoraPlan {
-  int rt;      // tiles of 16 rows per workgroup
-  int groups;  // workgroups that share a tile's distinct adapters
-  int ct;      // tiles of 16 rows of A per workgroup (first product)
+  int few;     // the first product row by row
+  int groups;  // workgroups that share a tile's work items
   int splits;  // parts of K
-  int blocks;  // blocks of 32 columns per wave (second product)
+  int blocks;  // blocks of 128 columns per workgroup (second product)
 };
-LoraPlan lora_plan(int rows, int batch, int K, int columns) {
+LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0) {
   LoraPlan p;
-  p.rt = rows > 256 ? 4 : 1;
-  p.groups = p.rt > 1 ? 1 : batch < 16 ? batch : 16;
-  p.ct = p.rt > 1 ? 4 : 1;
-  const int64_t tiles = ((int64_t)rows + 16 * p.rt - 1) / (16 * p.rt);
-  const int64_t wgs = tiles * p.groups * ((columns + 16 * p.ct - 1) / (16 * p.ct));
-  // a wave keeps 256 of K at least
-  int64_t s = 1024 / wgs;
-  if (s > K / 1024) s = K / 1024;
-  p.splits = s < 1 ? 1 : s > 16 ? 16 : (int)s;
-  p.blocks = p.rt > 1 ? 8 : 2;
+  // Up to 256 rows row by row (us against tiles of 64 rows: 128 rows of 200 adapters of
+  // rank 64 60 : 72, of one adapter 17 : 24; 300 rows of 4 adapters of rank 8 21.5 :
+  // 19.4, of rank 64 43 : 23).
+  p.few = rows <= 256;
+  p.groups = !p.few ? 1 : batch < 64 ? batch : 64;
+  const int64_t tiles = ((int64_t)rows + 63) / 64, width = p.few ? 16 : 64;
+  const int64_t wgs = tiles * p.groups * ((columns + width - 1) / width);
+  if (p.few) {
+    // about 1024 workgroups, of which those without an item leave at once, and 1024 of K
+    // to each (64 tokens of 40 adapters: 10.9 us, 12.9 with 2048, 19.3 with 4096)
+    int64_t s = 1024 / wgs;
+    if (s > K / 1024) s = K / 1024;
+    p.splits = s < 1 ? 1 : s > 16 ? 16 : (int)s;
+  } else {
+    // rounds of two workgroups per CU, and 1.5 % of one for every part that is written
+    // and read back (6400 rows of 192 columns: 129 us in one part, 117 in five)
+    double best = 1e30;
+    for (int s = 1; s == 1 || (s <= 16 && s * 512 <= K); ++s) {
+      const double cost = (double)((wgs * s + 511) / 512) / s + 0.015 * s;
+      if (cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
+  }
+  // about 1280 workgroups (64 tokens of 40 adapters: 20.2 us, 21.6 with 640, 25.9 with
+  // 2048; prompts 117, 120 with 768, 118 with 2048)
+  const int64_t blocks = (int64_t)((N + 127) / 128) * tiles * p.groups / 1280;
+  p.blocks = blocks < 1 ? 1 : blocks > 8 ? 8 : (int)blocks;
   return p;
 }
 
 __device__ inline u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
 }
-__device__ inline void store16(rsrc_t r, u32x4 v, uint32_t voff, uint32_t soff) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, voff, soff, 0);
-}
+// (The offset is added up here: behind a 128-bit store with a scalar offset the compiler
+// may rewrite the first data register in the very next instruction, and that value then
+// reached memory now and then; without one it keeps the distance.)
+__device__ inline void store16(rsrc_t r, u32x4 v, uint32_t off) { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0); }
 
 // Adapter of row row0 + lane (lane < TM): -1 for none, -2 outside every sequence.
-// The wave finds the first row's sequence and counts, for every row, the offsets
-// of the next 64 sequences that do not lie behind it.
+// The wave finds the first row's sequence and walks the offsets of those behind it
+// that begin in the tile.
 template <int TM>
 __device__ inline int tile_adapters(const LoraArgs& a, int row0, int lane) {
   const KvSeqs& s = a.seqs;
@@ -63,19 +86,20 @@ __device__ inline int tile_adapters(const LoraArgs& a, int row0, int lane) {
   } else {
     int first = kv_find_seq(s, row0, 1, 1, 0, lane);
     first = __builtin_amdgcn_readfirstlane(first < 0 ? 0 : first);
-    const int off = first + lane <= s.batch ? kv_row_offset(s, first + lane) : 0x7FFFFFFF;
-    bool beyond = false;
-    for (int i = 0; i < TM; ++i) {
-      const int n = __popcll(__ballot(off <= row0 + i));
-      beyond |= n == 64;
-      if (lane == i) seq = first + n - 1;  // (first - 1 where nothing is: before the first offset)
-      if (n == 0 && lane == i) seq = -1;
-    }
-    if (beyond) {  // more than 63 sequences without rows among them
+    const int row = row0 + lane, off = first + lane <= s.batch ? kv_row_offset(s, first + lane) : 0x7FFFFFFF;
+    uint64_t inside = __ballot(off < row0 + TM);
+    if (inside >> 63) {  // more than 63 sequences begin in the tile, most of them without rows
       for (int i = 0; i < TM; ++i) {
         int b = kv_find_seq(s, row0 + i, 1, 1, 0, lane);
         if (b >= 0 && row0 + i >= kv_row_offset(s, s.batch)) b = -1;
         if (lane == i) seq = b;
+      }
+    } else {
+      seq = -1;
+      while (inside) {
+        const int i = __builtin_ctzll(inside);
+        inside &= inside - 1;
+        if (row >= __builtin_amdgcn_readlane(off, i)) seq = first + i;
       }
     }
     if (seq >= s.batch || row0 + lane >= s.rows) seq = -1;
@@ -85,287 +109,558 @@ __device__ inline int tile_adapters(const LoraArgs& a, int row0, int lane) {
   return id < 0 || id >= a.num ? -1 : id;
 }
 __device__ inline int adapter_rank(const LoraArgs& a, int id) {
-  const int r = a.ranks ? a.ranks[id] : a.rank;
+  int r = a.rank;
+  asm("" : "+s"(r));  // (keeps the compiler from choosing between two addresses by a flat load)
+  if (a.ranks) r = a.ranks[id];
   return __builtin_amdgcn_readfirstlane(r < 0 ? 0 : r > a.rank ? a.rank : r);
 }
 
-// f(adapter) for the distinct values (from `least` on) among the first TM lanes'
-// ids: every `of`-th of them, from the `at`-th on.
-template <int TM, typename F>
-__device__ inline void each_adapter(int ids, int lane, int least, int at, int of, F&& f) {
-  uint64_t left = __ballot(lane < TM && ids >= least);
-  for (int g = 0; left; ++g) {
+// f(adapter, first) for the distinct values (from `least` on) among the 64 lanes' ids and
+// every PER of the rows that have one (0: all of them together): every `of`-th of these
+// items, from the `at`-th on.
+template <int PER, typename F>
+__device__ inline void each_adapter(int ids, int least, int at, int of, F&& f) {
+  uint64_t left = __ballot(ids >= least);
+  for (int skip = at; left;) {
     const int cur = __builtin_amdgcn_readlane(ids, __builtin_ctzll(left));
-    left &= ~__ballot(ids == cur);
-    if (g % of == at) f(cur);
+    const uint64_t same = __ballot(ids == cur);
+    left &= ~same;
+    const int items = PER ? (__popcll(same) + PER - 1) / (PER ? PER : 1) : 1;
+    for (; skip < items; skip += of) f(cur, skip * PER);
+    skip -= items;
   }
 }
 
-// v = x A^T, RT x CT tiles to a workgroup, its four waves (and the parts) split K.
-template <int DT, int RT, int CT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a, int splits) {
-  constexpr int G = RT == 1 ? 4 : 1;  // steps of 32 along K that are loaded together
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
-  const int row0 = blockIdx.x * 16 * RT, C = a.slices * a.rank;
-  const int split = blockIdx.y % splits, col0 = blockIdx.y / splits * 16 * CT;
-  const int ids = tile_adapters<16 * RT>(a, row0, lane);
-  int mine[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) mine[r] = __shfl(ids, 16 * r + c, 64);
-  const int left = a.seqs.rows - row0, tile_rows = left < 16 * RT ? left : 16 * RT;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+// 16 products of 4 x 4 numbers along 4 of K each: lane 4 b + i gives row i of the
+// first and column i of the second operand of product b, four entries of K, and gets
+// column i of its result: result i of lane i is what its own operands give.
+template <int DT>
+__device__ inline f4 mfma4(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, f4 c) {
+  const u32x2 a = {a0, a1}, b = {b0, b1};
+  if constexpr (DT == F16)
+    return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(h4, a), __builtin_bit_cast(h4, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s4, a), __builtin_bit_cast(s4, b), c, 0, 0, 0);
+}
+// sum over the 16 lanes of a row
+__device__ inline float sum_row(float v) {
+  auto ror = [&](auto n) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + decltype(n)::value, 0xf, 0xf, true));
+  };
+  ror(std::integral_constant<int, 8>{});
+  ror(std::integral_constant<int, 4>{});
+  ror(std::integral_constant<int, 2>{});
+  ror(std::integral_constant<int, 1>{});
+  return v;
+}
+
+// v = x A^T for few rows: 16 rows of A for the rows of x that share the adapter, up to
+// four of them to a workgroup.  The work is to read A: consecutive lanes take consecutive 16 bytes (a
+// load is 256 bytes of four rows), every lane multiplies its entries of A and x, and the
+// lanes are added up at the end.  (As operands of the 16-row product a load would be 64
+// bytes of sixteen rows at a stride of 16 lanes: 18.2 us instead of 10.8 for 64 tokens of
+// 40 adapters.)  The four waves (and the parts) split K.
+template <int DT>
+__global__ __launch_bounds__(256, 3) void lora_shrink_rows_kernel(const LoraArgs a, int splits) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = blockIdx.x * 64, C = a.slices * a.rank;
+  const int split = blockIdx.y % splits, col0 = blockIdx.y / splits * 16;
+  const int ids = tile_adapters<64>(a, row0, lane);
+  const int left = a.seqs.rows - row0, tile_rows = __builtin_amdgcn_readfirstlane(left < 64 ? left : 64);
   const rsrc_t xr = make_rsrc(a.x + (int64_t)row0 * a.K, (uint32_t)tile_rows * a.K * 2);
-  // this wave's steps of 32 G
   const int units = a.K / 128, part = split * 4 + wave, parts = splits * 4;
   const int k0 = (int)((int64_t)units * part / parts) * 128, k1 = (int)((int64_t)units * (part + 1) / parts) * 128;
-  __shared__ f4 red[4][RT * CT][64];
+  __shared__ float red[4][4][16];  // [wave][row of x][row of A]
 
-  each_adapter<16 * RT>(ids, lane, 0, blockIdx.z, gridDim.z, [&](int cur) {
+  each_adapter<4>(ids, 0, blockIdx.z, gridDim.z, [&](int cur, int before) {
     const int rank = adapter_rank(a, cur);
-    uint32_t xo[RT], ao[CT];
-    bool any = false;
+    // rows of A past the rank are not read (rank is a multiple of 8: eight of the 16 rows
+    // lie in one slice)
+    const int n0 = rank - col0 % a.rank, n1 = rank - (col0 + 8) % a.rank;
+    if (n0 <= 0 && (n1 <= 0 || col0 + 8 >= C)) return;
+    uint32_t ao[4];
 #pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      const int j = col0 + 16 * t + c;
-      const bool ok = j < C && j % a.rank < rank;
-      any |= ok;
-      ao[t] = ok ? ((uint32_t)j * a.K + 8 * h) * 2 : kOutOfRange;
+    for (int r = 0; r < 4; ++r) {
+      const int j = 4 * r + (lane >> 4);
+      const bool ok = col0 + j < C && (j & 7) < (r < 2 ? n0 : n1);
+      ao[r] = ok ? ((uint32_t)(col0 + j) * a.K + 8 * (lane & 15)) * 2 : kOutOfRange;
     }
-    if (!__any(any)) return;  // (the same in every wave)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) xo[r] = mine[r] == cur ? ((uint32_t)(16 * r + c) * a.K + 8 * h) * 2 : kOutOfRange;
     const rsrc_t ar = make_rsrc(a.a + (int64_t)cur * C * a.K, (uint32_t)C * a.K * 2);
-    f4 acc[RT][CT] = {};
-    u32x4 xf[2][G][RT], af[2][G][CT];
-    auto load = [&](int b, int k) {
+    uint64_t mask = __ballot(ids == cur);
+    for (int i = 0; i < before; ++i) mask &= mask - 1;
+    auto product = [&](auto tg) {
+      constexpr int TG = decltype(tg)::value, D = TG == 1 ? 4 : 2;
+      uint32_t xo[TG];
+      int row[TG];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
+      for (int t = 0; t < TG; ++t) {
+        row[t] = mask ? __builtin_ctzll(mask) : -1;
+        mask &= mask - 1;
+        xo[t] = row[t] >= 0 ? ((uint32_t)row[t] * a.K + 8 * (lane & 15)) * 2 : kOutOfRange;
+      }
+      f4 acc[4][TG] = {};
+      // a ring of D units of 128 along K: all but one in flight while that one is
+      // multiplied (past the end of the range the loads read nothing)
+      u32x4 af[D][4], xf[D][TG];
+      auto load = [&](int b, int k) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t) af[b][g][t] = load16(ar, ao[t], (k + 32 * g) * 2);
+        for (int r = 0; r < 4; ++r) af[b][r] = load16(ar, ao[r] | (k < k1 ? 0u : kOutOfRange), k * 2);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) xf[b][g][r] = load16(xr, xo[r], (k + 32 * g) * 2);
+        for (int t = 0; t < TG; ++t) xf[b][t] = load16(xr, xo[t] | (k < k1 ? 0u : kOutOfRange), k * 2);
+      };
+      auto multiply = [&](int b) {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+              acc[r][t] = mfma4<DT>(af[b][r][q], af[b][r][q + 1], xf[b][t][q], xf[b][t][q + 1], acc[r][t]);
+      };
+      int k = k0;
+      if (k < k1) {
+#pragma unroll
+        for (int u = 0; u < D - 1; ++u) load(u, k + 128 * u);
+      }
+      for (; k + 128 * (D - 1) < k1; k += 128 * D)
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+          load((u + D - 1) % D, k + 128 * (u + D - 1));
+          multiply(u);
+        }
+#pragma unroll
+      for (int u = 0; u < D - 1; ++u)
+        if (k + 128 * u < k1) multiply(u);
+      __syncthreads();  // (the last product's sums are read)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < TG; ++t) {
+          const f4 v = acc[r][t];
+          const float own = lane & 2 ? (lane & 1 ? v[3] : v[2]) : (lane & 1 ? v[1] : v[0]);
+          const float s = sum_row(own);
+          if ((lane & 15) == 0) red[wave][t][4 * r + (lane >> 4)] = s;
+        }
+      __syncthreads();
+      if (threadIdx.x < 16 * TG) {
+        const int t = threadIdx.x >> 4, j = threadIdx.x & 15;
+        float v = (red[0][t][j] + red[1][t][j]) + (red[2][t][j] + red[3][t][j]);
+        if ((j & 7) >= (j < 8 ? n0 : n1)) v = 0.f;  // (0 x is not 0 for every x)
+        int to = row[0];
+#pragma unroll
+        for (int o = 1; o < TG; ++o) to = t == o ? row[o] : to;
+        if (to >= 0 && col0 + j < C) a.part[((int64_t)split * a.seqs.rows + row0 + to) * C + col0 + j] = v;
       }
     };
-    auto multiply = [&](int b) {
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int t = 0; t < CT; ++t) acc[r][t] = mfma16<DT>(af[b][g][t], xf[b][g][r], acc[r][t]);
-    };
-    if (k0 < k1) {
-      load(0, k0);
-      for (int k = k0; k < k1; k += 64 * G) {
-        if (k + 32 * G < k1) load(1, k + 32 * G);
-        multiply(0);
-        if (k + 32 * G >= k1) break;
-        if (k + 64 * G < k1) load(0, k + 64 * G);
-        multiply(1);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) red[wave][r * CT + t][lane] = acc[r][t];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        const int i = r * CT + t;
-        if (i % 4 != wave) continue;
-        const f4 v = (red[0][i][lane] + red[1][i][lane]) + (red[2][i][lane] + red[3][i][lane]);
-        const int j = col0 + 16 * t + 4 * h;
-        if (mine[r] == cur && j < C)
-          *(f4*)(a.part + ((int64_t)split * a.seqs.rows + row0 + 16 * r + c) * C + j) = v;
-      }
-    __syncthreads();
+    if (mask & (mask - 1)) product(std::integral_constant<int, 4>{});
+    else product(std::integral_constant<int, 1>{});
   });
 }
 
-// 16-bit words of 8 entries, those from `n` on cleared
-__device__ inline u32x4 keep_first(u32x4 w, int n) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (n <= 2 * q) w[q] = 0;
-    else if (n == 2 * q + 1) w[q] &= 0xFFFFu;
-  }
-  return w;
+// A buffer resource as the four words make_rsrc puts into it.
+__device__ inline u32x4 words_of(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+// 16 bytes per lane into LDS (lane l writes lds[l]; lds is wave-uniform).  By
+// hand, because of what the compiler does behind its own form of it: it waits for
+// all such loads in flight before any LDS read that it cannot tell from them.
+// The waits are barrier_behind's.
+__device__ inline void load_lds(u32x4 r, const void* lds, uint32_t voff, uint32_t soff) {
+  const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
+  uint32_t kept;  // m0 is the compiler's
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(kept) : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(voff), "s"(r), "s"(soff) : "memory");
 }
 
-// out = y + scale v B^T; KC: blocks of 32 of the rank.
-template <int DT, int RT, int KC>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a, int splits, int blocks) {
+// Barrier of a workgroup that waits until at most n vector memory operations of
+// this wave are outstanding and all its LDS reads are done (s_waitcnt, gfx9
+// encoding).  __syncthreads would wait for every LDS-destination load in flight.
+template <int N>
+__device__ inline void barrier_behind() {
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// v = x A^T for many rows: 64 rows of x and 64 of A, 64 of K at a time, in a ring of four
+// stages in LDS that LDS-destination loads fill, three of them in flight.  A load takes
+// 128 consecutive bytes of eight rows by consecutive lanes (operands loaded straight
+// into registers, 64 bytes of sixteen rows at a stride of 16 lanes, took 55 us instead
+// of 34 for 6400 rows of 192 columns); 16-byte chunk j of a row lies at j ^ (row % 8), so that the operands are read without
+// bank conflicts.  A wave multiplies all the rows by 16 of A.
+template <int DT>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a, int splits) {
+  constexpr int S = 4, LOADS = 4;  // stages; loads of a wave for one, two of x and two of A
+  __shared__ u32x4 stage[S][8 * 128];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
-  const int row0 = blockIdx.x * 16 * RT, C = a.slices * a.rank;
-  const int ids = tile_adapters<16 * RT>(a, row0, lane);
-  int mine[RT];
+  const int row0 = blockIdx.x * 64, C = a.slices * a.rank;
+  const int split = blockIdx.y % splits, col0 = blockIdx.y / splits * 64;
+  const int ids = tile_adapters<64>(a, row0, lane);
+  const int left = a.seqs.rows - row0, tile_rows = __builtin_amdgcn_readfirstlane(left < 64 ? left : 64);
+  const u32x4 xr = words_of(a.x + (int64_t)row0 * a.K, (uint32_t)tile_rows * a.K * 2);
+  const int units = a.K / 64;
+  const int u0 = (int)((int64_t)units * split / splits), u1 = (int)((int64_t)units * (split + 1) / splits);
+
+  each_adapter<0>(ids, 0, blockIdx.z, gridDim.z, [&](int cur, int) {
+    const int rank = adapter_rank(a, cur);
+    const u32x4 ar = words_of(a.a + (int64_t)cur * C * a.K, (uint32_t)C * a.K * 2);
+    // rows of others and past the rank are not loaded: what lies in their places only
+    // reaches results that are not kept
+    const int lr = lane >> 3;
+    const uint32_t lk = (uint32_t)((lane & 7) ^ lr) * 16;
+    uint32_t off[LOADS];
+    bool any = false;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) mine[r] = __shfl(ids, 16 * r + c, 64);
-  const int left = a.seqs.rows - row0, tile_rows = left < 16 * RT ? left : 16 * RT;
+    for (int i = 0; i < LOADS; ++i) {
+      const int q = wave + 4 * i;
+      if (i < 2) {
+        const int row = 8 * q + lr;
+        off[i] = __shfl(ids, row, 64) == cur ? (uint32_t)row * a.K * 2 + lk : kOutOfRange;
+      } else {
+        const int j = col0 + 8 * (q - 8) + lr;
+        const bool ok = j < C && j % a.rank < rank;
+        any |= ok;
+        off[i] = ok ? (uint32_t)j * a.K * 2 + lk : kOutOfRange;
+      }
+    }
+    if (!__syncthreads_or(any)) return;  // (also: the last adapter's stages are read)
+    auto issue = [&](int u) {
+      const u32x4* to = stage[(u - u0) % S];
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) load_lds(i < 2 ? xr : ar, to + (wave + 4 * i) * 64, off[i], (uint32_t)u * 128);
+    };
+    f4 acc[4] = {};
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      if (u0 + i < u1) issue(u0 + i);
+    for (int u = u0; u < u1; ++u) {
+      // stage u is there for all, and stage u - 1 has been read by all
+      if (u + 2 < u1) barrier_behind<2 * LOADS>();
+      else if (u + 1 < u1) barrier_behind<LOADS>();
+      else barrier_behind<0>();
+      if (u + S - 1 < u1) issue(u + S - 1);
+      const u32x4* from = stage[(u - u0) % S];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = (4 * k + h) ^ (c & 7);
+        const u32x4 af = from[(64 + 16 * wave + c) * 8 + at];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = mfma16<DT>(af, from[(16 * r + c) * 8 + at], acc[r]);
+      }
+    }
+    const int j = col0 + 16 * wave + 4 * h, past = rank - j % a.rank;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f4 v = acc[r];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)  // (0 x is not 0 for every x)
+        if (q >= past) v[q] = 0.f;
+      if (__shfl(ids, 16 * r + c, 64) == cur && j < C)
+        *(f4*)(a.part + ((int64_t)split * a.seqs.rows + row0 + 16 * r + c) * C + j) = v;
+    }
+  });
+}
+
+// 8 entries of v times a power of two as the sum of two 16-bit numbers.
+template <int DT>
+__device__ inline void two_parts(f4 v0, f4 v1, float up, u32x4& hi, u32x4& lo) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const f4 v = q < 2 ? v0 : v1;
+    const float x0 = v[2 * (q % 2)] * up, x1 = v[2 * (q % 2) + 1] * up;
+    const uint32_t w = pack2<DT>(x0, x1);
+    const float h0 = act_lo<DT>(w), h1 = act_hi<DT>(w);
+    hi[q] = w;
+    // (an infinity is whole in its first part)
+    lo[q] = pack2<DT>(__builtin_isinf(h0) ? 0.f : x0 - h0, __builtin_isinf(h1) ? 0.f : x1 - h1);
+  }
+}
+__device__ inline float largest(f4 a, f4 b) {
+  float m = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m = fmaxf(m, fmaxf(fabsf(a[q]), fabsf(b[q])));
+  return m;
+}
+// fp16: the power of two that takes a row's largest to 2^13 .. 2^14, and the one back,
+// both normal numbers
+__device__ inline void powers(float m, float& up, float& down) {
+  int e = (int)(__float_as_uint(m) >> 23) - 127;
+  e = e < -100 ? -100 : e > 120 ? 13 : e;  // (tiny; an infinity or NaN is left as it is)
+  up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+  down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+}
+
+// A row's v as it enters the second product (lane (c, h): entries 32 k + 8 h .. + 7 of
+// lane c's row), the parts of K added up; returns the power of two that undoes its own.
+template <int DT, int KC>
+__device__ inline float split_v(const LoraArgs& a, int splits, int row, bool own, int slice, int rank, int h, u32x4* hi,
+                                u32x4* lo) {
+  const int C = a.slices * a.rank;
+  f4 v[KC][2] = {};
+  if (own) {
+    const float* part = a.part + (int64_t)row * C + slice * a.rank + 8 * h;
+    const int64_t next = (int64_t)a.seqs.rows * C;
+    constexpr int P = 4 / KC;  // parts that are loaded together
+    for (int p = 0; p < splits; p += P, part += P * next) {
+      f4 w[P][KC][2] = {};
+#pragma unroll
+      for (int o = 0; o < P; ++o)
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (p + o < splits && 32 * k + 8 * h + 4 * i < rank) w[o][k][i] = *(const f4*)(part + o * next + 32 * k + 4 * i);
+#pragma unroll
+      for (int o = 0; o < P; ++o)
+#pragma unroll
+        for (int k = 0; k < KC; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) v[k][i] += w[o][k][i];
+    }
+  }
+  float up = 1.f, down = 1.f;
+  if constexpr (DT == F16) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) m = fmaxf(m, largest(v[k][0], v[k][1]));
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    powers(m, up, down);
+  }
+#pragma unroll
+  for (int k = 0; k < KC; ++k) two_parts<DT>(v[k][0], v[k][1], up, hi[k], lo[k]);
+  return down;
+}
+
+// The same once for all workgroups that will use it, where they are many: 16 rows of one
+// slice, 16 lanes to a row.  The parts go to [row][slice][first, second][rank], the
+// powers behind them.
+template <int DT>
+__global__ __launch_bounds__(256) void lora_split_kernel(const LoraArgs a, int splits) {
+  const int row0 = blockIdx.x * 16, slice = blockIdx.y, C = a.slices * a.rank, i = threadIdx.x & 15, r = threadIdx.x >> 4;
+  const int id = __shfl(tile_adapters<16>(a, row0, threadIdx.x & 63), r, 64);
+  if (id < 0) return;  // (the same in the 16 lanes)
+  const int64_t next = (int64_t)a.seqs.rows * C;
+  const int rank = a.ranks ? a.ranks[id] : a.rank, row = row0 + r;
+  f4 v[2] = {};
+  const float* part = a.part + (int64_t)row * C + slice * a.rank + 8 * i;
+  for (int p = 0; p < splits; p += 4, part += 4 * next) {
+    f4 w[4][2] = {};
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (p + o < splits && 8 * i + 4 * e < rank && 8 * i < a.rank) w[o][e] = *(const f4*)(part + o * next + 4 * e);
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) v[e] += w[o][e];
+  }
+  float up = 1.f, down = 1.f;
+  if constexpr (DT == F16) {
+    float m = largest(v[0], v[1]);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    powers(m, up, down);
+  }
+  u32x4 hi, lo;
+  two_parts<DT>(v[0], v[1], up, hi, lo);
+  if (8 * i < a.rank) {
+    u32x4* to = (u32x4*)a.v + ((int64_t)row * a.slices + slice) * (a.rank >> 2) + i;
+    to[0] = hi;
+    to[a.rank >> 3] = lo;
+  }
+  if (i == 0) a.down[(int64_t)row * a.slices + slice] = down;
+}
+
+// out = y + scale v B^T; KC: blocks of 32 of the rank.  A workgroup takes 64 rows and
+// `blocks` blocks of 128 columns of one slice.  B goes through LDS: consecutive threads
+// load consecutive 16 bytes of it (chunk s of a block lies at s ^ (s / rank % 8), which
+// spreads the operands over the banks), and column 8 j + t is column j of tile t, so that
+// the results of the eight tiles are eight consecutive columns of four rows in a lane:
+// y is read and out written 256 consecutive bytes at a time.  (With 64 bytes of sixteen
+// rows a load, B straight from memory: 91 us instead of 76 for the prompts.)  Many rows:
+// a wave to 16 of them, all eight tiles.  Few: the waves share up to 16 rows of an
+// adapter and take two tiles each.
+template <int DT, bool FEW, int KC>
+__global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const LoraArgs a, int splits, int blocks) {
+  constexpr int NT = FEW ? 2 : 8, NL = 2 * KC;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
+  const int row0 = blockIdx.x * 64, R8 = a.rank >> 3, magic = (65535 + R8) / R8;  // x / R8 = x magic >> 16, x < 2048
+  int slice = 0, first = 0, end = a.ends[0], chunk = blockIdx.y;
+  for (;;) {
+    const int n = (end - first + 128 * blocks - 1) / (128 * blocks);
+    if (chunk < n) break;
+    chunk -= n;
+    first = end;
+    end = a.ends[++slice];
+  }
+  const int base0 = first + chunk * blocks * 128, stop = base0 + blocks * 128 < end ? base0 + blocks * 128 : end;
+  const int ids = tile_adapters<64>(a, row0, lane);
+  const int left = a.seqs.rows - row0, tile_rows = __builtin_amdgcn_readfirstlane(left < 64 ? left : 64);
   const rsrc_t yr = make_rsrc(a.y + (int64_t)row0 * a.N, (uint32_t)tile_rows * a.N * 2);
   const rsrc_t outr = make_rsrc(a.out + (int64_t)row0 * a.N, (uint32_t)tile_rows * a.N * 2);
-  // this wave's blocks of 32 columns: no block spans two slices
-  const int first = (blockIdx.y * 4 + wave) * blocks;
-  int s0 = 0, b0 = first;
-  while (s0 < a.slices) {
-    const int w = a.ends[s0] - (s0 ? a.ends[s0 - 1] : 0), n = (w + 31) >> 5;
-    if (b0 < n) break;
-    b0 -= n;
-    ++s0;
-  }
-  if (s0 == a.slices) return;
+  __shared__ u32x4 stage[2][512 * KC];
+  int buf = 0;
 
-  each_adapter<16 * RT>(ids, lane, a.y == a.out ? 0 : -1, blockIdx.z, gridDim.z, [&](int cur) {
+  each_adapter<FEW ? 16 : 0>(ids, a.y == a.out ? 0 : -1, blockIdx.z, gridDim.z, [&](int cur, int before) {
     const int rank = cur < 0 ? 0 : adapter_rank(a, cur);
     const float scale = cur < 0 ? 0.f : a.scales[cur];
     const rsrc_t br = make_rsrc(a.b + (int64_t)(cur < 0 ? 0 : cur) * a.N * a.rank, (uint32_t)a.N * a.rank * 2);
-    uint32_t yo[RT];
+    uint32_t bo[NL];
+    int bn[NL];  // column of the chunk this thread loads
 #pragma unroll
-    for (int r = 0; r < RT; ++r) yo[r] = ((uint32_t)(16 * r + c) * a.N + 8 * h) * 2;
-    const uint32_t bo = ((uint32_t)(8 * (c >> 2) + (c & 3)) * a.rank + 8 * h) * 2;
-    u32x4 hi[RT][KC], lo[RT][KC];
-    float back[RT];
-    u32x4 yv[RT], bv[2][KC];
-    int s = s0, base = (s0 ? a.ends[s0 - 1] : 0) + 32 * b0, have = -1;
-    auto load = [&] {
+    for (int l = 0; l < NL; ++l) {
+      const int at = l * 256 + threadIdx.x, s = at ^ (((at >> 3) * magic >> 16) & 7), n = s * magic >> 16;
+      const bool ok = at < 128 * R8 && 8 * (s - n * R8) < rank;
+      bo[l] = (uint32_t)s * 16;
+      bn[l] = ok ? n : 1 << 24;
+    }
+    u32x4 keep[KC];  // B past the rank is not used, whatever it holds
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int k = 0; k < KC; ++k) {
+      const int n = rank - 32 * k - 8 * h;
 #pragma unroll
-        for (int k = 0; k < KC; ++k)
-          bv[i][k] = load16(br, base + 8 * (c >> 2) + (c & 3) + 4 * i < a.ends[s] && 32 * k + 8 * h < rank
-                                    ? bo + (uint32_t)(4 * i * a.rank + 32 * k) * 2 : kOutOfRange,
-                            (uint32_t)base * a.rank * 2);
+      for (int q = 0; q < 4; ++q) keep[k][q] = n <= 2 * q ? 0u : n == 2 * q + 1 ? 0xFFFFu : 0xFFFFFFFFu;
+    }
+    const uint64_t mask = __ballot(ids == cur);
+    int list = 0;
+    if constexpr (FEW) {  // the adapter's rows in a row
+      const int at = __popcll(mask & ((1ull << lane) - 1));
+      list = __builtin_amdgcn_ds_permute(4 * ((mask >> lane) & 1 ? at : 63 - (lane - at)), lane);
+    }
+    // the row of lane c, and those of the results (4 h + q)
+    int row;
+    if constexpr (FEW) {
+      row = __shfl(list, (before + c) & 63, 64);
+      if (before + c >= __popcll(mask)) row = -1;
+    } else {
+      row = 16 * wave + c;
+      if (__shfl(ids, row, 64) != cur) row = -1;
+    }
+    uint32_t yo[4];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        yv[r] = load16(yr, mine[r] == cur && base + 8 * h < a.ends[s] ? yo[r] : kOutOfRange, (uint32_t)base * 2);
+    for (int q = 0; q < 4; ++q) {
+      const int r = __shfl(row, 4 * h + q, 64);
+      yo[q] = r >= 0 ? ((uint32_t)r * a.N + 8 * c + (FEW ? 2 * wave : 0)) * 2 : kOutOfRange;
+    }
+    u32x4 bv[NL], yv[4];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+        bv[l] = load16(br, base + bn[l] < end ? bo[l] : kOutOfRange, (uint32_t)base * a.rank * 2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t o = base + 8 * c < end ? yo[q] : kOutOfRange;
+        if constexpr (FEW) yv[q][0] = __builtin_amdgcn_raw_buffer_load_b32(yr, o, (uint32_t)base * 2, 0);
+        else yv[q] = load16(yr, o, (uint32_t)base * 2);
+      }
     };
-    load();
-    for (int n = 0; n < blocks; ++n) {
-      if (have != s) {
-        have = s;
+    load(base0);
+    u32x4 hi[KC], lo[KC];
+    float down = 1.f;
+    if constexpr (FEW) {
+      down = split_v<DT, KC>(a, splits, row0 + row, row >= 0, slice, rank, h, hi, lo);
+    } else {
+      const int64_t at = (int64_t)(row0 + (row < 0 ? 0 : row)) * a.slices + slice;
+      if (DT == F16 && row >= 0) down = a.down[at];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          f4 v[KC][2] = {};
-          for (int p = 0; p < splits; ++p) {
-            const rsrc_t pr = make_rsrc(a.part + ((int64_t)p * a.seqs.rows + row0) * C, (uint32_t)tile_rows * C * 4);
-#pragma unroll
-            for (int k = 0; k < KC; ++k)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint32_t at = (uint32_t)((16 * r + c) * C + s * a.rank + 32 * k + 8 * h + 4 * i) * 4;
-                v[k][i] += __builtin_bit_cast(f4, load16(pr, mine[r] == cur && 32 * k + 8 * h + 4 * i < rank ? at : kOutOfRange, 0));
-              }
-          }
-          float m = 0.f;
-#pragma unroll
-          for (int k = 0; k < KC; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              // (past the rank nothing was written)
-              const float x = 32 * k + 8 * h + e < rank ? v[k][e / 4][e % 4] : 0.f;
-              v[k][e / 4][e % 4] = x;
-              m = fmaxf(m, fabsf(x));
-            }
-          back[r] = scale;
-          float up = 1.f;
-          if constexpr (DT == F16) {
-            m = fmaxf(m, __shfl_xor(m, 16, 64));
-            m = fmaxf(m, __shfl_xor(m, 32, 64));
-            // exponent of the largest to 2^13: 2^(13 - e), 2^(e - 13), both normal numbers
-            int e = (int)(__float_as_uint(m) >> 23) - 127;
-            e = e < -100 ? -100 : e > 120 ? 13 : e;  // (tiny; an infinity or NaN is left as it is)
-            up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-            back[r] = scale * __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-          }
-#pragma unroll
-          for (int k = 0; k < KC; ++k)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float x0 = v[k][q / 2][2 * (q % 2)] * up, x1 = v[k][q / 2][2 * (q % 2) + 1] * up;
-              const uint32_t w = pack2<DT>(x0, x1);
-              const float h0 = act_lo<DT>(w), h1 = act_hi<DT>(w);
-              hi[r][k][q] = w;
-              // (an infinity is whole in its first part)
-              lo[r][k][q] = pack2<DT>(__builtin_isinf(h0) ? 0.f : x0 - h0, __builtin_isinf(h1) ? 0.f : x1 - h1);
-            }
+      for (int k = 0; k < KC; ++k) {
+        hi[k] = lo[k] = u32x4{0u, 0u, 0u, 0u};
+        if (row >= 0 && 32 * k + 8 * h < rank) {
+          const u32x4* from = (const u32x4*)a.v + at * (a.rank >> 2) + 4 * k + h;
+          hi[k] = from[0];
+          lo[k] = from[a.rank >> 3];
         }
       }
-      u32x4 yc[RT], bc[2][KC];
+    }
+    down *= scale;
+    float back[4];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) yc[r] = yv[r];
+    for (int q = 0; q < 4; ++q) back[q] = __shfl(down, 4 * h + q, 64);
+    for (int base = base0; base < stop; base += 128, buf ^= 1) {
+      u32x4 yc[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int q = 0; q < 4; ++q) yc[q] = yv[q];
 #pragma unroll
-        for (int k = 0; k < KC; ++k) bc[i][k] = a.ranks ? keep_first(bv[i][k], rank - 32 * k - 8 * h) : bv[i][k];
-      const int at = base, end = a.ends[s];
-      base += 32;
-      if (base >= end) base = end, ++s;
-      const bool more = n + 1 < blocks && s < a.slices;
-      if (more) load();
+      for (int l = 0; l < NL; ++l) stage[buf][l * 256 + threadIdx.x] = bv[l];
+      if (base + 128 < stop) load(base + 128);
+      __syncthreads();  // (the block before the last one has been read by all)
+      f4 d[NT] = {};
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        f4 d[2] = {};
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < KC; ++k)
+        for (int k = 0; k < KC; ++k) {
+          const u32x4 bt = stage[buf][((8 * c + t + (FEW ? 2 * wave : 0)) * R8 + 4 * k + h) ^ (c & 7)] & keep[k];
+          d[t] = mfma16<DT>(lo[k], bt, d[t]);
+          d[t] = mfma16<DT>(hi[k], bt, d[t]);
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) d[i] = mfma16<DT>(bc[i][k], lo[r][k], d[i]);
+      for (int q = 0; q < 4; ++q) {
+        u32x4 o = yc[q];
+        if (rank > 0) {  // (no adapter: a copy)
 #pragma unroll
-        for (int k = 0; k < KC; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) d[i] = mfma16<DT>(bc[i][k], hi[r][k], d[i]);
-        u32x4 o;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          o[q] = pack2<DT>(__builtin_fmaf(d[q / 2][2 * (q % 2)], back[r], act_lo<DT>(yc[r][q])),
-                           __builtin_fmaf(d[q / 2][2 * (q % 2) + 1], back[r], act_hi<DT>(yc[r][q])));
-        if (rank == 0) o = yc[r];  // (no adapter: a copy)
-        store16(outr, o, mine[r] == cur && at + 8 * h < end ? yo[r] : kOutOfRange, (uint32_t)at * 2);
+          for (int w = 0; w < NT / 2; ++w)
+            o[w] = pack2<DT>(__builtin_fmaf(d[2 * w][q], back[q], act_lo<DT>(yc[q][w])),
+                             __builtin_fmaf(d[2 * w + 1][q], back[q], act_hi<DT>(yc[q][w])));
+        }
+        const uint32_t to = (base + 8 * c < end ? yo[q] : kOutOfRange) + (uint32_t)base * 2;
+        if constexpr (FEW) __builtin_amdgcn_raw_buffer_store_b32(o[0], outr, to, 0, 0);
+        else store16(outr, o, to);
       }
-      if (!more) break;
     }
   });
 }
 
-template <int DT, int RT, int CT>
-void shrink(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
-  const int tiles = (a.seqs.rows + 16 * RT - 1) / (16 * RT), cols = (a.slices * a.rank + 16 * CT - 1) / (16 * CT);
-  hipLaunchKernelGGL((lora_shrink_kernel<DT, RT, CT>), dim3(tiles, cols * p.splits, p.groups), dim3(256), 0, s, a, p.splits);
-}
-template <int DT, int RT, int KC>
-void expand(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
-  const int tiles = (a.seqs.rows + 16 * RT - 1) / (16 * RT);
-  int n = 0;
-  for (int i = 0; i < a.slices; ++i) n += (a.ends[i] - (i ? a.ends[i - 1] : 0) + 31) / 32;
-  hipLaunchKernelGGL((lora_expand_kernel<DT, RT, KC>), dim3(tiles, (n + 4 * p.blocks - 1) / (4 * p.blocks), p.groups), dim3(256),
-                     0, s, a, p.splits, p.blocks);
+template <int DT, bool FEW, int KC>
+void expand(const LoraArgs& a, const LoraPlan& p, int tiles, hipStream_t s) {
+  int chunks = 0;
+  for (int i = 0; i < a.slices; ++i)
+    chunks += (a.ends[i] - (i ? a.ends[i - 1] : 0) + 128 * p.blocks - 1) / (128 * p.blocks);
+  hipLaunchKernelGGL((lora_expand_kernel<DT, FEW, KC>), dim3(tiles, chunks, p.groups), dim3(256), 0, s, a, p.splits, p.blocks);
 }
 
 template <int DT>
 wq_status launch(const LoraArgs& a, hipStream_t s) {
-  const LoraPlan p = lora_plan(a.seqs.rows, a.seqs.batch, a.K, a.slices * a.rank);
-  const int kc = (a.rank + 31) / 32;
-  if (p.rt == 1) {
-    shrink<DT, 1, 1>(a, p, s);
-    if (kc == 1) expand<DT, 1, 1>(a, p, s);
-    else if (kc == 2) expand<DT, 1, 2>(a, p, s);
-    else expand<DT, 1, 4>(a, p, s);
+  const int columns = a.slices * a.rank;
+  const LoraPlan p = lora_plan(a.seqs.rows, a.seqs.batch, a.K, columns, a.N);
+  const int tiles = (a.seqs.rows + 63) / 64, kc = (a.rank + 31) / 32;
+  const int width = p.few ? 16 : 64;
+  const dim3 grid(tiles, (columns + width - 1) / width * p.splits, p.groups), block(256);
+  if (p.few) hipLaunchKernelGGL((lora_shrink_rows_kernel<DT>), grid, block, 0, s, a, p.splits);
+  else hipLaunchKernelGGL((lora_shrink_kernel<DT>), grid, block, 0, s, a, p.splits);
+  if (!p.few) hipLaunchKernelGGL((lora_split_kernel<DT>), dim3((a.seqs.rows + 15) / 16, a.slices), block, 0, s, a, p.splits);
+  if (p.few) {
+    if (kc == 1) expand<DT, true, 1>(a, p, tiles, s);
+    else if (kc == 2) expand<DT, true, 2>(a, p, tiles, s);
+    else expand<DT, true, 4>(a, p, tiles, s);
   } else {
-    shrink<DT, 4, 4>(a, p, s);
-    if (kc == 1) expand<DT, 4, 1>(a, p, s);
-    else if (kc == 2) expand<DT, 4, 2>(a, p, s);
-    else expand<DT, 2, 4>(a, p, s);
+    if (kc == 1) expand<DT, false, 1>(a, p, tiles, s);
+    else if (kc == 2) expand<DT, false, 2>(a, p, tiles, s);
+    else expand<DT, false, 4>(a, p, tiles, s);
   }
   return launch_status();
 }
 
 }  // namespace
 
+// Parts of v; for many rows then its two 16-bit parts and the powers of two.
+static size_t part_bytes(const LoraPlan& p, int rows, int columns) { return (size_t)p.splits * rows * columns * 4; }
 size_t lora_workspace_bytes(int rows, int batch, int K, int rank, int slices) {
-  return (size_t)lora_plan(rows, batch, K, rank * slices).splits * rows * rank * slices * 4;
+  const LoraPlan p = lora_plan(rows, batch, K, rank * slices);
+  return part_bytes(p, rows, rank * slices) + (p.few ? 0 : (size_t)rows * slices * (4 * rank + 4));
 }
 
-wq_status launch_lora(const LoraArgs& a, int dt, hipStream_t s) {
+wq_status launch_lora(const LoraArgs& args, int dt, hipStream_t s) {
+  LoraArgs a = args;
+  const int rows = a.seqs.rows, columns = a.slices * a.rank;
+  a.v = (uint16_t*)a.part + part_bytes(lora_plan(rows, a.seqs.batch, a.K, columns), rows, columns) / 2;
+  a.down = (float*)(a.v + (size_t)rows * columns * 2);
   return dt == F16 ? launch<F16>(a, s) : launch<BF16>(a, s);
 }
 
