@@ -187,9 +187,14 @@ def test_resize_refusals(L):
         assert resize_call(L, **{name: None}) == 1, name
     assert resize_call(L, table=(1 << 20) + 2) == 2
     assert resize_call(L, slots=(8 << 20) + 4) == 2
-    assert resize_call(L, ws=None) == 4
-    assert resize_call(L, ws_bytes=8) == 4
-    assert resize_call(L, ws=(9 << 20) + 8) == 2
+    # (a small step needs no scratch; an output that overlaps is looked at behind it)
+    assert wq.wq_kv_resize_workspace_bytes(4, 8, 32, 16) == 0
+    assert resize_call(L, ws=None, ws_bytes=0, cu=2 << 20) == 1
+    need = wq.wq_kv_resize_workspace_bytes(4, 8, 32, 1 << 14)
+    assert need > 0
+    assert resize_call(L, rows=1 << 14, ws=None, slots=16 << 20) == 4
+    assert resize_call(L, rows=1 << 14, ws_bytes=need - 1, slots=16 << 20) == 4
+    assert resize_call(L, rows=1 << 14, ws=(9 << 20) + 8, slots=16 << 20) == 2
     assert resize_call(L, want=2 << 20) == 1                  # lengths over wanted lengths
     assert resize_call(L, cu=(2 << 20) + 8) == 1
     assert resize_call(L, pos=(1 << 20) + 124) == 1           # over the table's last entry

@@ -1,13 +1,21 @@
 // wq_kv_pages.hip -- sequences of the paged cache grow and shrink on the GPU.
 //
 // A sequence of n tokens holds ceil(n / P) pages.  Three sums over the sequences
-// -- pages that go back, pages that are taken, new rows -- number every page of a
-// call in the order (sequence, entry); the f-th page taken is the f-th given
-// back, what is left over on either side comes from or goes to the stack's place
-// top - 1 - f, top counting the pages given back.  One thread then moves the f-th
-// page of both kinds (it alone reads that table entry, or that place of the
+// -- pages that go back, pages that are taken, new rows -- number every page and
+// row of a call in the order (sequence, entry).  The f-th page taken is the f-th
+// given back; what is left over on either side comes from or goes to the stack's
+// place top - 1 - f, top counting the pages given back.  One thread moves the
+// f-th page of both kinds (it alone reads that table entry, or that place of the
 // stack, and it alone writes the other), so nothing waits on anything but the
 // sums, and a sequence that grows and shrinks again leaves the stack as it was.
+//
+// Behind the sums everything follows from them and the wanted lengths, so the
+// lengths are written at once: a sequence's taken entries are its last ones, the
+// entries given back those behind its last.
+//
+// A step of few sequences and rows is one workgroup, its sums in LDS: the time is
+// a launch and the chain lengths -> sums -> pages -> rows.  Prompts take three
+// launches, one thread to a page and to four rows.
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -48,116 +56,188 @@ __device__ inline int owner(const int32_t* off, int n, int f) {
   return lo;
 }
 
-// One workgroup does all of it.
-__global__ __launch_bounds__(kThreads) void resize_kernel(const PagesArgs a) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, B = a.batch;
-  int32_t *back_off = a.offsets, *take_off = back_off + (B + 1), *row_off = take_off + (B + 1);
+// The sums before this thread's sequences and in all, over a workgroup of kThreads.
+__device__ inline void sum_before(Sums own, Sums& before, Sums& total) {
   __shared__ Sums part[kThreads / 64];
-  __shared__ int bad_any;
-  if (t == 0) bad_any = 0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Sums run = own;
+  if (__any((own.back | own.taken | own.rows) != 0))
+    for (int d = 1; d < 64; d <<= 1) {
+      const Sums p = up(run, d);
+      if (lane >= d) run = run + p;
+    }
+  if (lane == 63) part[wave] = run;
+  __syncthreads();
+  before = {run.back - own.back, run.taken - own.taken, run.rows - own.rows};
+  total = {0, 0, 0};
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w == wave) before = before + total;
+    total = total + part[w];
+  }
+}
+__device__ inline Sums change(const PagesArgs& a, const Lens& l) {
+  const int d = pages_of(a, l.want) - pages_of(a, l.old);
+  return {d < 0 ? -d : 0, d > 0 ? d : 0, l.want > l.old ? l.want - l.old : 0};
+}
+
+// Offsets of the sequences' pages given back and taken and of their new rows.
+struct Offsets {
+  int32_t *back, *taken, *rows;  // [batch + 1] each
+};
+__device__ inline Offsets offsets_in(int32_t* p, int batch) { return {p, p + (batch + 1), p + 2 * (batch + 1)}; }
+
+// The sums, the verdict, lengths and counts.  `sums` come back as zeros where nothing
+// may change.  Every thread has read what it needs of lens and counts before any writes.
+__device__ inline Sums settle(const PagesArgs& a, const Offsets& o, int64_t& top) {
+  const int t = threadIdx.x, B = a.batch;
   const int per = (B + kThreads - 1) / kThreads, b0 = t * per < B ? t * per : B, b1 = b0 + per < B ? b0 + per : B;
   Sums own = {0, 0, 0};
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     const Lens l = lens_of(a, b);
     bad |= l.bad;
-    const int d = pages_of(a, l.want) - pages_of(a, l.old);
-    own = own + Sums{d < 0 ? -d : 0, d > 0 ? d : 0, l.want > l.old ? l.want - l.old : 0};
+    own = own + change(a, l);
   }
-  Sums run = own;
-  for (int d = 1; d < 64; d <<= 1) {
-    const Sums p = up(run, d);
-    if (lane >= d) run = run + p;
-  }
-  if (lane == 63) part[wave] = run;
-  __syncthreads();
-  if (bad) bad_any = 1;
-  Sums before = {0, 0, 0}, total = {0, 0, 0};
-  for (int w = 0; w < kThreads / 64; ++w) {
-    if (w < wave) before = before + part[w];
-    total = total + part[w];
-  }
-  Sums at = before + run;
-  at = {at.back - own.back, at.taken - own.taken, at.rows - own.rows};
   int count = a.counts[0];
   count = count < 0 ? 0 : count > a.num_pages ? a.num_pages : count;
-  __syncthreads();
-  const int64_t top = count + total.back;
+  Sums at, total;
+  sum_before(own, at, total);
+  bad = __syncthreads_or(bad);
+  top = count + total.back;
   int status = 0;
-  if (bad_any || top > a.num_pages || total.rows > (1 << 24)) status = -1;
+  if (bad || top > a.num_pages || total.rows > (1 << 24)) status = -1;
   else if (total.taken > top) status = (int)(total.taken - top);
-  __syncthreads();  // every thread has read counts[0] and the lengths' verdict
-  if (t == 0) a.counts[1] = status;
-  if (status != 0) {
-    if (a.cu_q)
-      for (int b = t; b <= B; b += kThreads) a.cu_q[b] = 0;
-    for (int r = t; r < a.rows; r += kThreads) {
-      if (a.positions) a.positions[r] = -1;
-      if (a.slots) a.slots[r] = -1;
-    }
-    return;
+  if (status) {
+    total = at = {0, 0, 0};
+    top = count;
   }
   for (int b = b0; b < b1; ++b) {
-    back_off[b] = (int)at.back;
-    take_off[b] = (int)at.taken;
-    row_off[b] = (int)at.rows;
+    o.back[b] = (int)at.back;
+    o.taken[b] = (int)at.taken;
+    o.rows[b] = (int)at.rows;
     if (a.cu_q) a.cu_q[b] = (int)at.rows;
+    if (status) continue;
     const Lens l = lens_of(a, b);
-    const int d = pages_of(a, l.want) - pages_of(a, l.old);
-    at = at + Sums{d < 0 ? -d : 0, d > 0 ? d : 0, l.want > l.old ? l.want - l.old : 0};
+    at = at + change(a, l);
+    a.lens[b] = l.want;
   }
   if (t == 0) {
-    back_off[B] = (int)total.back;
-    take_off[B] = (int)total.taken;
-    row_off[B] = (int)total.rows;
+    o.back[B] = (int)total.back;
+    o.taken[B] = (int)total.taken;
+    o.rows[B] = (int)total.rows;
     if (a.cu_q) a.cu_q[B] = (int)total.rows;
-    a.counts[0] = (int)(top - total.taken);
+    if (status == 0) a.counts[0] = (int)(top - total.taken);
+    a.counts[1] = status;
   }
-  __syncthreads();
-  const int nback = (int)total.back, ntake = (int)total.taken;
-  for (int f = t; f < (nback > ntake ? nback : ntake); f += kThreads) {
-    int page;
-    if (f < nback) {
-      const int b = owner(back_off, B, f);
-      const Lens l = lens_of(a, b);
-      int32_t* from = a.table + (int64_t)b * a.max_pages + pages_of(a, l.want) + (f - back_off[b]);
-      page = *from;
-      *from = -1;
-    } else {
-      page = a.free_pages[top - 1 - f];
-    }
-    if (f < ntake) {
-      const int b = owner(take_off, B, f);
-      const Lens l = lens_of(a, b);
-      a.table[(int64_t)b * a.max_pages + pages_of(a, l.old) + (f - take_off[b])] = page;
-    } else {
-      a.free_pages[top - 1 - f] = page;
-    }
+  return total;
+}
+
+// The f-th page given back and the f-th taken.
+__device__ inline void move_page(const PagesArgs& a, const Offsets& o, int nback, int ntake, int64_t top, int f) {
+  int page;
+  if (f < nback) {
+    const int b = owner(o.back, a.batch, f);
+    int32_t* from = a.table + (int64_t)b * a.max_pages + pages_of(a, a.want[b]) + (f - o.back[b]);
+    page = *from;
+    *from = -1;
+  } else {
+    page = a.free_pages[top - 1 - f];
   }
+  if (f < ntake) {
+    const int b = owner(o.taken, a.batch, f);
+    a.table[(int64_t)b * a.max_pages + pages_of(a, a.want[b]) - (o.taken[b + 1] - f)] = page;
+  } else {
+    a.free_pages[top - 1 - f] = page;
+  }
+}
+
+// Position and slot of new row r of sequence b (-1: none).
+__device__ inline void map_row(const PagesArgs& a, const Offsets& o, int b, int r, int& pos, int64_t& slot) {
+  pos = -1;
+  slot = -1;
+  if (b < 0) return;
+  pos = a.want[b] - (o.rows[b + 1] - r);
+  const int page = a.table[(int64_t)b * a.max_pages + (pos >> a.page_shift)];
+  slot = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+}
+
+// One workgroup does all of it (batch up to kThreads).
+__global__ __launch_bounds__(kThreads) void resize_kernel(const PagesArgs a) {
+  __shared__ int32_t sums[3 * (kThreads + 1)];
+  const Offsets o = offsets_in(sums, a.batch);
+  int64_t top;
+  const Sums total = settle(a, o, top);
   __syncthreads();
-  const int new_rows = (int)total.rows;
-  for (int r = t; r < a.rows; r += kThreads) {
-    int pos = -1;
-    int64_t slot = -1;
-    if (r < new_rows) {
-      const int b = owner(row_off, B, r);
-      pos = lens_of(a, b).old + (r - row_off[b]);
-      const int page = a.table[(int64_t)b * a.max_pages + (pos >> a.page_shift)];
-      slot = ((int64_t)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-    }
+  const int nback = (int)total.back, ntake = (int)total.taken, new_rows = (int)total.rows;
+  for (int f = threadIdx.x; f < (nback > ntake ? nback : ntake); f += kThreads) move_page(a, o, nback, ntake, top, f);
+  __syncthreads();
+  for (int r = threadIdx.x; r < a.rows; r += kThreads) {
+    int pos;
+    int64_t slot;
+    map_row(a, o, r < new_rows ? owner(o.rows, a.batch, r) : -1, r, pos, slot);
     if (a.positions) a.positions[r] = pos;
     if (a.slots) a.slots[r] = slot;
   }
-  __syncthreads();
-  for (int b = t; b < B; b += kThreads) a.lens[b] = a.want[b];
 }
+
+// The same in three launches.
+__global__ __launch_bounds__(kThreads) void resize_sums_kernel(const PagesArgs a) {
+  int64_t top;
+  settle(a, offsets_in(a.offsets, a.batch), top);
+  if (threadIdx.x == 0) a.offsets[3 * (a.batch + 1)] = (int)top;
+}
+__global__ __launch_bounds__(256) void resize_move_kernel(const PagesArgs a) {
+  const Offsets o = offsets_in(a.offsets, a.batch);
+  const int nback = o.back[a.batch], ntake = o.taken[a.batch], top = a.offsets[3 * (a.batch + 1)];
+  for (int f = blockIdx.x * 256 + threadIdx.x; f < (nback > ntake ? nback : ntake); f += gridDim.x * 256)
+    move_page(a, o, nback, ntake, top, f);
+}
+__global__ __launch_bounds__(256) void resize_map_kernel(const PagesArgs a) {
+  const Offsets o = offsets_in(a.offsets, a.batch);
+  const int new_rows = o.rows[a.batch], r0 = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (r0 >= a.rows) return;
+  int b = r0 < new_rows ? owner(o.rows, a.batch, r0) : -1;
+  int pos[4];
+  int64_t slot[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + i;
+    if (r >= new_rows) b = -1;
+    else
+      while (o.rows[b + 1] <= r) ++b;  // (the last offset lies behind every new row)
+    map_row(a, o, b, r, pos[i], slot[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (r0 + i < a.rows) {
+      if (a.positions) a.positions[r0 + i] = pos[i];
+      if (a.slots) a.slots[r0 + i] = slot[i];
+    }
+}
+
+// One workgroup up to this many sequences and new rows.  Two changes of 64 sequences, us in
+// one : three launches: 33 rows 12.3 : 16.2, 2850 14.1 : 16.9, 4795 15.4 : 17.7, 11003 19.9
+// : 18.3 (300 sequences and 375000 rows each: 1630 : 33).  It moves 1024 pages at a time,
+// so a call of few rows that ends many long sequences at once takes longer in it.
+constexpr int kOneBatch = kThreads, kOneRows = 8192;
 
 }  // namespace
 
-size_t pages_workspace_bytes(int batch, int, int, int) { return (size_t)(batch + 1) * 12; }
+size_t pages_workspace_bytes(int batch, int, int, int rows) {
+  return batch <= kOneBatch && rows <= kOneRows ? 0 : (size_t)(batch + 1) * 12 + 4;
+}
 
 wq_status launch_resize(const PagesArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(resize_kernel, dim3(1), dim3(kThreads), 0, s, a);
+  if (a.batch <= kOneBatch && a.rows <= kOneRows) {
+    hipLaunchKernelGGL(resize_kernel, dim3(1), dim3(kThreads), 0, s, a);
+    return launch_status();
+  }
+  hipLaunchKernelGGL(resize_sums_kernel, dim3(1), dim3(kThreads), 0, s, a);
+  const int64_t most = (int64_t)a.batch * a.max_pages < a.num_pages ? (int64_t)a.batch * a.max_pages : a.num_pages;
+  const int64_t wgs = (most + 255) / 256;
+  if (wgs) hipLaunchKernelGGL(resize_move_kernel, dim3((int)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, a);
+  if (a.rows && (a.positions || a.slots))
+    hipLaunchKernelGGL(resize_map_kernel, dim3((a.rows + 1023) / 1024), dim3(256), 0, s, a);
   return launch_status();
 }
 

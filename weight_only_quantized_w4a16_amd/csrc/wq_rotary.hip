@@ -14,6 +14,10 @@
 // time (two 16-byte loads that lie rotary_dim / 2 apart, or 8 adjacent
 // channels).  Every thread reads what it writes before it does, so outputs may
 // be written over inputs.
+//
+// What bounds it: memory for prompts (7001 rows of 32 + 8 heads of 128, three axes,
+// 143 MB: 31 us, 4.6 TB/s; a copy runs at 4.75), for single tokens a launch and the
+// chain offsets -> length -> rows (64 rows of 64 + 8 heads: 3.7 us).
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -55,17 +59,19 @@ __device__ inline bool row_position(const KvSeqs& s, int row, int lane, int& pos
   return row >= q.row0 && row - q.row0 < q.n;
 }
 
-// One wave to a row.
-template <int DT, bool ADJ>
+// W waves to a row, 4 / W rows to a workgroup.
+template <int DT, bool ADJ, int W>
 __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
-  __shared__ f2 cs[4][kMaxHalf];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = blockIdx.x * 4 + wave;
+  constexpr int THREADS = 64 * W;
+  __shared__ f2 cs_all[4 / W][kMaxHalf];
+  const int t = threadIdx.x % THREADS;
+  const int row = blockIdx.x * (4 / W) + threadIdx.x / THREADS;
+  f2* cs = cs_all[threadIdx.x / THREADS];
   bool live = row < a.seqs.rows;
   int pos = 0;
-  if (live && !a.positions) live = row_position(a.seqs, row, lane, pos);
+  if (live && !a.positions) live = row_position(a.seqs, row, threadIdx.x & 63, pos);
   if (live) {
-    for (int i = lane; i < a.half; i += 64) {
+    for (int i = t; i < a.half; i += THREADS) {
       int p = pos;
       if (a.positions) {
         int ax = a.axis ? a.axis[i] : 0;
@@ -73,7 +79,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
         p = a.positions[ax * a.ld_pos + row];
       }
       const uint64_t u = (uint64_t)(int64_t)p * a.turns[i];
-      cs[wave][i] = turn((uint32_t)(u >> 32)) * a.factor;
+      cs[i] = turn((uint32_t)(u >> 32)) * a.factor;
     }
   }
   __syncthreads();
@@ -81,7 +87,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
   const int per = a.half >> (ADJ ? 2 : 3);                // items of turning pairs in a head
   const int rest = (a.head_dim - 2 * a.half) >> 3;        // 16-byte chunks that are copied
   const int items = per + rest, total = (a.heads[0] + a.heads[1]) * items;
-  for (int it = lane; it < total; it += 64) {
+  for (int it = t; it < total; it += THREADS) {
     int head = it / items;
     const int c = it % items;
     const int which = head >= a.heads[0];
@@ -96,9 +102,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
       u32x4 o;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f2 t = cs[wave][4 * c + q];
-        const float p = act_lo<DT>(v[q]), r = act_hi<DT>(v[q]);
-        o[q] = pack2<DT>(p * t[0] - r * t[1], p * t[1] + r * t[0]);
+        const f2 r = cs[4 * c + q];
+        const float p0 = act_lo<DT>(v[q]), p1 = act_hi<DT>(v[q]);
+        o[q] = pack2<DT>(p0 * r[0] - p1 * r[1], p0 * r[1] + p1 * r[0]);
       }
       *(u32x4*)(y + 8 * c) = o;
     } else {
@@ -106,10 +112,10 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
       u32x4 o, n;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const f2 t = cs[wave][8 * c + 2 * q], s = cs[wave][8 * c + 2 * q + 1];
-        const float p0 = act_lo<DT>(v[q]), p1 = act_hi<DT>(v[q]), r0 = act_lo<DT>(w[q]), r1 = act_hi<DT>(w[q]);
-        o[q] = pack2<DT>(p0 * t[0] - r0 * t[1], p1 * s[0] - r1 * s[1]);
-        n[q] = pack2<DT>(p0 * t[1] + r0 * t[0], p1 * s[1] + r1 * s[0]);
+        const f2 r = cs[8 * c + 2 * q], s = cs[8 * c + 2 * q + 1];
+        const float p0 = act_lo<DT>(v[q]), p1 = act_hi<DT>(v[q]), m0 = act_lo<DT>(w[q]), m1 = act_hi<DT>(w[q]);
+        o[q] = pack2<DT>(p0 * r[0] - m0 * r[1], p1 * s[0] - m1 * s[1]);
+        n[q] = pack2<DT>(p0 * r[1] + m0 * r[0], p1 * s[1] + m1 * s[0]);
       }
       *(u32x4*)(y + 8 * c) = o;
       *(u32x4*)(y + a.half + 8 * c) = n;
@@ -117,20 +123,25 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryArgs a) {
   }
 }
 
-template <int DT>
-wq_status launch(const RotaryArgs& a, int adjacent, hipStream_t s) {
-  const dim3 grid((a.seqs.rows + 3) / 4), block(256);
-  if (adjacent)
-    hipLaunchKernelGGL((rotary_kernel<DT, true>), grid, block, 0, s, a);
+template <int DT, bool ADJ>
+wq_status launch(const RotaryArgs& a, hipStream_t s) {
+  // Four waves to a row where it has work for them (32 + 8 heads of 128, one wave : four,
+  // us: 64 rows 4.5 : 3.2, 1024 rows 7.3 : 6.0, 8192 rows 36.7 : 33.0) or rows are few;
+  // else one (8 + 1 heads of 64: 1024 rows 3.1 : 3.4, 8192 rows 7.1 : 11.6; 64 rows 2.9
+  // : 2.7).
+  const int chunks = (a.half >> (ADJ ? 2 : 3)) + ((a.head_dim - 2 * a.half) >> 3);
+  if ((a.heads[0] + a.heads[1]) * chunks >= 256 || a.seqs.rows <= 256)
+    hipLaunchKernelGGL((rotary_kernel<DT, ADJ, 4>), dim3(a.seqs.rows), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((rotary_kernel<DT, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rotary_kernel<DT, ADJ, 1>), dim3((a.seqs.rows + 3) / 4), dim3(256), 0, s, a);
   return launch_status();
 }
 
 }  // namespace
 
 wq_status launch_rotary(const RotaryArgs& a, int dt, int adjacent, hipStream_t s) {
-  return dt == F16 ? launch<F16>(a, adjacent, s) : launch<BF16>(a, adjacent, s);
+  if (dt == F16) return adjacent ? launch<F16, true>(a, s) : launch<F16, false>(a, s);
+  return adjacent ? launch<BF16, true>(a, s) : launch<BF16, false>(a, s);
 }
 
 }  // namespace wq

@@ -67,22 +67,26 @@ def wq_lora(x: torch.Tensor, bank: LoraBank, adapters: torch.Tensor, y: torch.Te
     outside every sequence of cu_q are left as they were in `out` (undefined where this call allocates it)."""
     if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.shape[1] == bank.K and x.is_contiguous()):
         raise ValueError("x must be a contiguous [rows][K] tensor")
-    dt, dev, rows = _dt(x.dtype), x.device, x.shape[0]
-    if bank.a.dtype != x.dtype or bank.a.device != dev:
+    dtype, dev, rows = x.dtype, x.device, x.shape[0]
+    dt = _dt(dtype)
+    if bank.a.dtype != dtype or bank.a.device != dev:
         raise ValueError(f"the bank must be of x's dtype on its device, got {bank.a.dtype} on {bank.a.device}")
-    _check_tensor(y, "y", (x.dtype,), (rows, bank.N), dev)
+    shape = (rows, bank.N)
+    for t, name in ((y, "y"), (out, "out")):
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+                and t.device == dev) and not (t is None and name == "out"):
+            _check_tensor(t, name, (dtype,), shape, dev)
     if not (isinstance(adapters, torch.Tensor) and adapters.dim() == 1):
         raise ValueError("adapters must be a [batch] tensor")
     batch = adapters.shape[0]
-    _check_tensor(adapters, "adapters", (torch.int32,), (batch,), dev)
+    if not (adapters.dtype == torch.int32 and adapters.is_contiguous() and adapters.device == dev):
+        _check_tensor(adapters, "adapters", (torch.int32,), (batch,), dev)
     if cu_q is not None:
         _check_tensor(cu_q, "cu_q", (torch.int32,), (batch + 1,), dev)
     elif rows and (batch == 0 or rows % batch):
         raise ValueError(f"without cu_q every sequence has as many rows: {rows} rows of {batch} sequences")
     if rows and batch == 0:
         raise ValueError("rows need a sequence")
-    if out is not None:
-        _check_tensor(out, "out", (x.dtype,), (rows, bank.N), dev)
     L = lib()
     need = L.wq_lora_workspace_bytes(rows, batch, bank.K, bank.rank, bank.num_slices)
     if ws is not None and need:
@@ -92,7 +96,7 @@ def wq_lora(x: torch.Tensor, bank: LoraBank, adapters: torch.Tensor, y: torch.Te
     _check_cuda(x, "x")
     at = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, y, y.shape)
+        out = _empty(stream, y, shape)
     if need and ws is None:
         ws = _empty(stream, x, need, torch.uint8, scratch=True)
     rc = L.wq_lora(x.data_ptr(), dt, bank.a.data_ptr(), bank.b.data_ptr(), bank.scales.data_ptr(), _ptr(bank.ranks),

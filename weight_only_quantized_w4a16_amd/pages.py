@@ -68,7 +68,9 @@ def wq_kv_resize(pages: KVPages, want_lens: torch.Tensor, rows: int = 0, cu_q: O
     dev, (batch, max_pages) = table.device, table.shape
     if not (isinstance(rows, int) and rows >= 0):
         raise ValueError("rows must be a count")
-    _check_tensor(want_lens, "want_lens", (torch.int32,), (batch,), dev)
+    if not (isinstance(want_lens, torch.Tensor) and want_lens.dtype == torch.int32 and want_lens.shape == (batch,)
+            and want_lens.is_contiguous() and want_lens.device == dev):
+        _check_tensor(want_lens, "want_lens", (torch.int32,), (batch,), dev)
     for t, name, dtype, n in ((cu_q, "cu_q", torch.int32, batch + 1), (positions, "positions", torch.int32, rows),
                               (slots, "slots", torch.int64, rows)):
         if t is not None:

@@ -16,27 +16,28 @@ import torch
 from . import WQError, _check_cuda, _check_tensor, _dt, _empty, _need, _ptr, _stream, lib
 
 
-def _rows(x, name: str, dtype, dim: Optional[int], dev, heads: Optional[int], rows: Optional[int]):
-    """Address and elements between rows of x [rows][heads][dim] (a row contiguous)."""
-    if not (isinstance(x, torch.Tensor) and x.dim() == 3):
-        raise ValueError(f"{name} must be a [rows][heads][channels] tensor")
-    n, h, d = x.shape
-    sn, sh, sd = x.stride()
-    if n <= 1:
-        sn = h * d
-    at = x.data_ptr()
-    if ((dim is None or d == dim) and x.dtype == dtype and (rows is None or n == rows) and (heads is None or h == heads)
-            and x.device == dev and (n == 0 or h == 0 or d == 0 or ((sd == 1 or d == 1) and (h == 1 or sh == d)
-                                                                   and sn >= h * d and sn % 8 == 0 and at % 16 == 0))):
-        return at, sn
+def _rows(x, name: str, dtype, shape, dev) -> Tuple[int, int]:
+    """Address and elements between rows of x ([rows][channels] or [rows][heads][channels] of `shape`, a row contiguous)."""
+    # (these checks run on every call: the common case first, what is wrong is named only after it failed)
+    if isinstance(x, torch.Tensor) and x.shape == shape and x.dtype == dtype and x.device == dev:
+        at, sn = x.data_ptr(), x.stride(0)
+        if x.is_contiguous():
+            if at % 16 == 0:
+                return at, sn if shape[0] > 1 else shape[-1] * (shape[1] if len(shape) == 3 else 1)
+        else:
+            st = x.stride()
+            width = shape[-1] * (shape[1] if len(shape) == 3 else 1)
+            _need(st[-1] == 1 and (len(shape) == 2 or shape[1] == 1 or st[1] == shape[-1]),
+                  f"a row of {name} (its heads, their channels) must be contiguous")
+            _need(shape[0] <= 1 or (sn >= width and sn % 8 == 0),
+                  f"the row stride of {name} must be a multiple of 8 elements and hold a row")
+            if at % 16 == 0:
+                return at, sn if shape[0] > 1 else width
+        raise ValueError(f"{name} must be 16-byte aligned")
+    _need(isinstance(x, torch.Tensor), f"{name} must be a tensor")
     _need(x.dtype == dtype, f"{name} must have dtype {dtype}, got {x.dtype}")
-    _need(dim is None or d == dim, f"{name} must have {dim} channels, got {d}")
-    _need(heads is None or h == heads, f"{name} must have {heads} heads, got {h}")
-    _need(rows is None or n == rows, f"{name} must have {rows} rows, got {n}")
-    _need(x.device == dev, f"{name} must be on {dev}, got {x.device}")
-    _need(sd == 1 and (h == 1 or sh == d), f"the heads of a row of {name} must be contiguous")
-    _need(sn >= h * d and sn % 8 == 0, f"the row stride of {name} must be a multiple of 8 elements and hold a row")
-    raise ValueError(f"{name} must be 16-byte aligned")
+    _need(x.shape == shape, f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    raise ValueError(f"{name} must be on {dev}, got {x.device}")
 
 
 def wq_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -47,37 +48,34 @@ def wq_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
     x or residual themselves."""
     if not (isinstance(x, torch.Tensor) and x.dim() in (2, 3)):
         raise ValueError("x must be a [rows][channels] or [rows][heads][channels] tensor")
-    flat = x.dim() == 2
-
-    def three(t, name):
-        if not (isinstance(t, torch.Tensor) and t.dim() == x.dim()):
-            raise ValueError(f"{name} must be a tensor like x")
-        return t.unsqueeze(1) if flat else t
-
-    dt, dev = _dt(x.dtype), x.device
-    xs = three(x, "x")
-    x_at, ld_x = _rows(xs, "x", x.dtype, None, dev, None, None)
-    rows, heads, dim = xs.shape
-    _need(heads > 0 and dim > 0, "x must have channels")
-    _check_tensor(weight, "weight", (x.dtype,), (dim,), dev)
-    r_at, ld_r = (None, 0) if residual is None else _rows(three(residual, "residual"), "residual", x.dtype, dim, dev,
-                                                          heads, rows)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    dt = _dt(dtype)
+    rows, dim = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
+    if heads == 0 or dim == 0:
+        raise ValueError("x must have channels")
+    x_at, ld_x = _rows(x, "x", dtype, shape, dev)
+    if not (isinstance(weight, torch.Tensor) and weight.dtype == dtype and weight.shape == (dim,) and weight.is_contiguous()
+            and weight.device == dev):
+        _check_tensor(weight, "weight", (dtype,), (dim,), dev)
     if not (isinstance(eps, (int, float)) and eps > 0 and math.isfinite(eps)):
         raise ValueError(f"eps must be positive and finite, got {eps}")
-    _need(sum_out is None or residual is not None, "sum_out needs a residual")
+    r_at, ld_r, s_at, ld_s = None, 0, None, 0
+    if residual is not None:
+        r_at, ld_r = _rows(residual, "residual", dtype, shape, dev)
+        if sum_out is not None:
+            s_at, ld_s = _rows(sum_out, "sum_out", dtype, shape, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
     if out is not None:
-        y_at, ld_y = _rows(three(out, "out"), "out", x.dtype, dim, dev, heads, rows)
-    if sum_out is not None:
-        s_at, ld_s = _rows(three(sum_out, "sum_out"), "sum_out", x.dtype, dim, dev, heads, rows)
+        y_at, ld_y = _rows(out, "out", dtype, shape, dev)
     _check_cuda(x, "x")
     at = _stream(stream, dev)
     if out is None:
-        out = _empty(stream, x, x.shape)
+        out = _empty(stream, x, shape)
         y_at, ld_y = out.data_ptr(), heads * dim
-    if residual is None:
-        s_at, ld_s = None, 0
-    elif sum_out is None:
-        sum_out = _empty(stream, x, x.shape)
+    if residual is not None and sum_out is None:
+        sum_out = _empty(stream, x, shape)
         s_at, ld_s = sum_out.data_ptr(), heads * dim
     rc = lib().wq_rms_norm(x_at, ld_x, r_at, ld_r, weight.data_ptr(), eps, dt, y_at, ld_y, s_at, ld_s, rows, heads,
                            dim, at)
@@ -161,16 +159,19 @@ def wq_rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: Rotary, position
     outside every sequence of cu_q are left as they were in `out` (undefined where this call allocates it)."""
     if not (isinstance(q, torch.Tensor) and q.dim() == 3):
         raise ValueError("q must be a [rows][heads][head_dim] tensor")
-    dt, dev, D = _dt(q.dtype), q.device, plan.head_dim
-    q_at, ld_q = _rows(q, "q", q.dtype, D, dev, None, None)
-    rows, heads = q.shape[0], q.shape[1]
-    _need(heads > 0, "q must have heads")
-    if k is None:
-        k_at, ld_k, kv_heads = None, 0, 0
-    else:
-        k_at, ld_k = _rows(k, "k", q.dtype, D, dev, None, rows)
-        kv_heads = k.shape[1]
-        _need(kv_heads > 0, "k must have heads")
+    shape, dtype, dev, D = q.shape, q.dtype, q.device, plan.head_dim
+    dt = _dt(dtype)
+    rows, heads, d = shape
+    if d != D or heads == 0:
+        raise ValueError(f"q must have heads of {D} channels, got {tuple(shape)}")
+    q_at, ld_q = _rows(q, "q", dtype, shape, dev)
+    k_at, ld_k, kv_heads, ko_at, ld_ko = None, 0, 0, None, 0
+    if k is not None:
+        k_shape = k.shape if isinstance(k, torch.Tensor) else ()
+        if len(k_shape) != 3 or k_shape[0] != rows or k_shape[1] == 0 or k_shape[2] != D:
+            raise ValueError(f"k must be [{rows}][heads][{D}], got {tuple(k_shape)}")
+        k_at, ld_k = _rows(k, "k", dtype, k_shape, dev)
+        kv_heads = k_shape[1]
     if plan.turns.device != dev:
         raise ValueError("the plan and q must be on the same device")
     ld_pos = batch = 0
@@ -182,7 +183,8 @@ def wq_rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: Rotary, position
     else:
         _need(isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1, "positions or kv_lens [batch] are needed")
         batch = kv_lens.shape[0]
-        _check_tensor(kv_lens, "kv_lens", (torch.int32,), (batch,), dev)
+        if not (kv_lens.dtype == torch.int32 and kv_lens.is_contiguous() and kv_lens.device == dev):
+            _check_tensor(kv_lens, "kv_lens", (torch.int32,), (batch,), dev)
         if cu_q is not None:
             _check_tensor(cu_q, "cu_q", (torch.int32,), (batch + 1,), dev)
         elif rows and (batch == 0 or rows % batch):
@@ -191,22 +193,19 @@ def wq_rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: Rotary, position
             raise ValueError("rows need a sequence")
     if out is not None:
         q_out, k_out = out
-        qo_at, ld_qo = _rows(q_out, "out[0]", q.dtype, D, dev, heads, rows)
-        if k is None:
-            _need(k_out is None, "out[1] must be None without k")
-        else:
-            ko_at, ld_ko = _rows(k_out, "out[1]", q.dtype, D, dev, kv_heads, rows)
+        qo_at, ld_qo = _rows(q_out, "out[0]", dtype, shape, dev)
+        if k is not None:
+            ko_at, ld_ko = _rows(k_out, "out[1]", dtype, k_shape, dev)
+        elif k_out is not None:
+            raise ValueError("out[1] must be None without k")
     _check_cuda(q, "q")
     at = _stream(stream, dev)
     if out is None:
-        q_out = _empty(stream, q, q.shape)
+        q_out, k_out = _empty(stream, q, shape), None
         qo_at, ld_qo = q_out.data_ptr(), heads * D
-        k_out = None
         if k is not None:
-            k_out = _empty(stream, k, k.shape)
+            k_out = _empty(stream, k, k_shape)
             ko_at, ld_ko = k_out.data_ptr(), kv_heads * D
-    if k is None:
-        ko_at, ld_ko = None, 0
     rc = lib().wq_rotary(q_at, ld_q, k_at, ld_k, dt, plan.turns.data_ptr(), _ptr(plan.axis), plan.factor,
                          _ptr(positions), ld_pos, _ptr(kv_lens), _ptr(cu_q), qo_at, ld_qo, ko_at, ld_ko, rows, batch,
                          heads, kv_heads, D, plan.rotary_dim, int(plan.adjacent), plan.num_axes, at)
