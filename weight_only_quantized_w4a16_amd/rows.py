@@ -27,10 +27,10 @@ def _rows(x, name: str, dtype, shape, dev) -> Tuple[int, int]:
         else:
             st = x.stride()
             width = shape[-1] * (shape[1] if len(shape) == 3 else 1)
-            _need(st[-1] == 1 and (len(shape) == 2 or shape[1] == 1 or st[1] == shape[-1]),
-                  f"a row of {name} (its heads, their channels) must be contiguous")
-            _need(shape[0] <= 1 or (sn >= width and sn % 8 == 0),
-                  f"the row stride of {name} must be a multiple of 8 elements and hold a row")
+            if not (st[-1] == 1 and (len(shape) == 2 or shape[1] == 1 or st[1] == shape[-1])):
+                raise ValueError(f"a row of {name} (its heads, their channels) must be contiguous")
+            if shape[0] > 1 and (sn < width or sn % 8):
+                raise ValueError(f"the row stride of {name} must be a multiple of 8 elements and hold a row")
             if at % 16 == 0:
                 return at, sn if shape[0] > 1 else width
         raise ValueError(f"{name} must be 16-byte aligned")
@@ -177,8 +177,8 @@ def wq_rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: Rotary, position
     ld_pos = batch = 0
     if positions is not None:
         _need(kv_lens is None and cu_q is None, "either positions or kv_lens")
-        shape = (rows,) if positions.dim() == 1 else (plan.num_axes, rows)
-        _check_tensor(positions, "positions", (torch.int32,), shape, dev)
+        _check_tensor(positions, "positions", (torch.int32,), (rows,) if positions.dim() == 1 else (plan.num_axes, rows),
+                      dev)
         ld_pos = rows if positions.dim() == 2 else 0
     else:
         _need(isinstance(kv_lens, torch.Tensor) and kv_lens.dim() == 1, "positions or kv_lens [batch] are needed")
