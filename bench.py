@@ -54,6 +54,8 @@ KERNEL_SOURCES = ["wq_gemv.hip", "wq_decode.hpp", "wq_layout.hpp"]  # the domina
 ALL_SOURCES = ["wq_api.hip", "wq_common.hpp", "wq_decode.hpp", "wq_gemm.hip", "wq_gemv.hip", "wq_hadamard.hip",
                "wq_layout.hpp"]
 KV_SOURCES = ["wq_kv.hpp", "wq_kv_api.hip", "wq_kv_attention.hip", "wq_kv_rows.hip"]  # cache operators'
+LAYER_SOURCES = ["wq_checks.hpp", "wq_kv_pages.hip", "wq_layer.hpp", "wq_layer_api.hip", "wq_lora.hip", "wq_norm.hip",
+                 "wq_rotary.hip"]  # norms, rotary positions, adapters, page tables
 
 
 def parse():
@@ -89,10 +91,11 @@ def parse():
                         "adds a 256 MiB device copy (counter calibration)")
     p.add_argument("--profile-reps", type=int, default=40)
     p.add_argument("--operators", nargs="*", default=None, metavar="CASE",
-                   help="instead of the step: time the cases of perf/operators.py (the 4-bit cache, attention over it, "
-                        "epilogue products; all of them when none is named), graph-replayed")
+                   help="instead of the step: time the cases of perf/operators.py and perf/more_operators.py (the 4-bit "
+                        "cache, attention over it, epilogue products; norms, rotary positions, adapters, page tables; all "
+                        "of them when none is named), graph-replayed")
     p.add_argument("--profile-operator", default="", metavar="CASE",
-                   help="instead of the step: one case of perf/operators.py, warmed and run --profile-reps times")
+                   help="instead of the step: one of those cases, warmed and run --profile-reps times")
     return p.parse_args()
 
 
@@ -317,23 +320,26 @@ def run_profile_cases(args):
 
 
 def operator_cases():
+    """(module, case) of every measured operator case, the modules set to the package's own calls."""
     import importlib.util
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
-    return ops
+    found = []
+    for name in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        found += [(ops, case) for case in ops.listed()]
+    return found
 
 
 def run_operators(args):
-    """The measured cases of the cache operators and the epilogue product through the package, one JSON line each:
+    """The measured cases of the operators around the products through the package, one JSON line each:
     three states in turn, ten rounds captured in a HIP graph, median of 5 replays after the warm-up.  Bytes and FLOP
     are what the operator cannot do without."""
     import torch
     torch.cuda.set_device(0)
     stream = torch.cuda.current_stream()
-    ops = operator_cases()
-    for case in ops.listed():
+    for ops, case in operator_cases():
         if args.operators and case["name"] not in args.operators:
             continue
         states = [ops.prepare(case, seed) for seed in range(3)]
@@ -363,8 +369,7 @@ def run_operators(args):
 def run_profile_operator(args):
     import torch
     torch.cuda.set_device(0)
-    ops = operator_cases()
-    case = next(c for c in ops.listed() if c["name"] == args.profile_operator)
+    ops, case = next((o, c) for o, c in operator_cases() if c["name"] == args.profile_operator)
     st = ops.prepare(case, 0)
     warm_up(torch.cuda.current_stream(), lambda: [ops.run(st) for _ in range(10)])
     for _ in range(args.profile_reps):

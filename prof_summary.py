@@ -231,7 +231,7 @@ def main():
     sys.path.insert(0, ROOT)
     import bench
     print(f"Kernel sources sha256/16: GEMV {bench.kernel_hash()}, products {bench.kernel_hash(bench.ALL_SOURCES)}, "
-          f"cache {bench.kernel_hash(bench.KV_SOURCES)}\n")
+          f"cache {bench.kernel_hash(bench.KV_SOURCES)}, layer {bench.kernel_hash(bench.LAYER_SOURCES)}\n")
     (trace if args.kind == "trace" else pmc)(args)
 
 

@@ -248,6 +248,56 @@ def test_adapters_leave_other_rows(dtype, lead, tail):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new", [[1] + [0] * 100 + [1, 0, 2], [0] * 200 + [3] + [0] * 70, [200, 0, 150, 1, 40] + [0] * 80 + [5]])
+def test_adapters_of_sequences_without_rows(dtype, new):
+    """More empty sequences than a wave has lanes; few rows and many; in place and not, some without an adapter, an
+    adapter of rank 0, junk past the ranks."""
+    g = torch.Generator().manual_seed(len(new) + sum(new))
+    c = adapters_case(g, dtype, new, 256, [96, 48], 24, 5, True, 2, 3, junk=True)
+    x, y, ids, cu = c["x"].cuda(), c["y"].cuda(), i32(c["ids"]), i32(c["cu"])
+    out = torch.full_like(y, 7)
+    wq.wq_lora(x, c["bank"], ids, y, cu_q=cu, out=out)
+    end = c["T"] - 3
+    within(out[2:end], c["want"][2:end], c["bound"][2:end])
+    assert bool((out[:2] == 7).all()) and bool((out[end:] == 7).all())
+    wq.wq_lora(x, c["bank"], ids, y, cu_q=cu, out=y)
+    assert torch.equal(y[2:end], out[2:end])
+    plan = wq.wq_rotary_plan(64)
+    q = randn(g, c["T"], 3, 64).to(dtype)
+    lens = [n + 5 for n in new]
+    turned = q.cuda()
+    wq.wq_rotary(turned, None, plan, kv_lens=i32(lens), cu_q=cu, out=(turned, None))
+    at = [p for n in new for p in range(5, 5 + n)]
+    want, bound = _layer.rotary(q[2:end], torch.tensor([at]), [10000.0 ** (-i / 32) for i in range(32)], [0] * 32, False, 1.0)
+    within(turned[2:end], want, bound)
+    assert torch.equal(turned[:2].cpu(), q[:2]) and torch.equal(turned[end:].cpu(), q[end:])
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^31 elements: the last rows come out as they do alone."""
+    rows, width = 70000, 32768
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 10000):
+        x[i:i + 10000] = torch.randn(10000, width, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(width, generator=g, device="cuda").bfloat16()
+    tail = x[-50:].clone()
+    assert torch.equal(wq.wq_rms_norm(x, w)[-50:], wq.wq_rms_norm(tail, w))
+    plan = wq.wq_rotary_plan(128)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    a = wq.wq_rotary(x.view(rows, 256, 128), None, plan, positions=pos)[0][-50:]
+    assert torch.equal(a, wq.wq_rotary(tail.view(50, 256, 128), None, plan, positions=pos[-50:])[0])
+    bank = wq.LoraBank((torch.randn(2, 16, 256, generator=g, device="cuda") / 16).bfloat16(),
+                       torch.randn(2, width, 16, generator=g, device="cuda").bfloat16(), torch.ones(2, device="cuda"))
+    xs = torch.randn(rows, 256, generator=g, device="cuda").bfloat16()
+    ids = i32([0, 1])
+    got = wq.wq_lora(xs, bank, ids, x, cu_q=i32([0, rows - 50, rows]), out=x)[-50:]
+    # (the tail alone is summed in another order: within its bound)
+    want, bound = _layer.lora(xs[-50:].cpu(), tail.cpu(), bank.a.cpu()[:, None], bank.b.cpu(), [1.0, 1.0], [16, 16], (width,), [1] * 50)
+    within(got, want, bound)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_adapters_of_large_and_infinite_values(dtype):
     """x A^T past fp16's range, an infinity in one row, a NaN in another: the other rows hold."""
     g = torch.Generator().manual_seed(9)

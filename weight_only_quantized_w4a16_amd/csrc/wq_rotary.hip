@@ -130,7 +130,7 @@ wq_status launch(const RotaryArgs& a, hipStream_t s) {
   // else one (8 + 1 heads of 64: 1024 rows 3.1 : 3.4, 8192 rows 7.1 : 11.6; 64 rows 2.9
   // : 2.7).
   const int chunks = (a.half >> (ADJ ? 2 : 3)) + ((a.head_dim - 2 * a.half) >> 3);
-  if ((a.heads[0] + a.heads[1]) * chunks >= 256 || a.seqs.rows <= 256)
+  if (((a.heads[0] + a.heads[1]) * chunks >= 256 || a.seqs.rows <= 256) && a.seqs.rows < (1 << 24))  // (grid limit)
     hipLaunchKernelGGL((rotary_kernel<DT, ADJ, 4>), dim3(a.seqs.rows), dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((rotary_kernel<DT, ADJ, 1>), dim3((a.seqs.rows + 3) / 4), dim3(256), 0, s, a);
