@@ -83,6 +83,20 @@ __device__ inline int tile_adapters(const LoraArgs& a, int row0, int lane) {
   int seq = -1;
   if (!s.cu_q) {
     if (lane < TM && row0 + lane < s.rows) seq = (uint32_t)(row0 + lane) / (uint32_t)(s.rows / s.batch);
+  } else if (s.batch < 64) {  // all offsets at once, and the adapters with them
+    const int off = lane <= s.batch ? kv_row_offset(s, lane) : 0x7FFFFFFF;
+    const int each = lane < s.batch ? a.adapters[lane] : -1;
+    const int row = row0 + lane;
+    seq = __popcll(__ballot(off <= row0)) - 1;
+    uint64_t inside = __ballot(off > row0 && off < row0 + TM);
+    while (inside) {
+      const int i = __builtin_ctzll(inside);
+      inside &= inside - 1;
+      if (row >= __builtin_amdgcn_readlane(off, i)) seq = i;
+    }
+    const int id = __shfl(each, seq & 63, 64);
+    if (lane >= TM || row >= s.rows || seq < 0 || seq >= s.batch) return -2;
+    return id < 0 || id >= a.num ? -1 : id;
   } else {
     int first = kv_find_seq(s, row0, 1, 1, 0, lane);
     first = __builtin_amdgcn_readfirstlane(first < 0 ? 0 : first);
@@ -287,15 +301,16 @@ __device__ inline void barrier_behind() {
   asm volatile("" ::: "memory");
 }
 
-// v = x A^T for many rows: 64 rows of x and 64 of A, 64 of K at a time, in a ring of four
-// stages in LDS that LDS-destination loads fill, three of them in flight.  A load takes
+// v = x A^T for many rows: 64 rows of x and 64 of A, 64 of K at a time, in a ring of
+// three stages in LDS that LDS-destination loads fill, two of them in flight (two stages
+// 32 us, three 31, four 34 for 6400 rows of 192 columns: three leave room for three
+// workgroups on a CU).  A load takes
 // 128 consecutive bytes of eight rows by consecutive lanes (operands loaded straight
-// into registers, 64 bytes of sixteen rows at a stride of 16 lanes, took 55 us instead
-// of 34 for 6400 rows of 192 columns); 16-byte chunk j of a row lies at j ^ (row % 8), so that the operands are read without
+// into registers, 64 bytes of sixteen rows at a stride of 16 lanes, took 55 us); 16-byte chunk j of a row lies at j ^ (row % 8), so that the operands are read without
 // bank conflicts.  A wave multiplies all the rows by 16 of A.
 template <int DT>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a, int splits) {
-  constexpr int S = 4, LOADS = 4;  // stages; loads of a wave for one, two of x and two of A
+  constexpr int S = 3, LOADS = 4;  // stages; loads of a wave for one, two of x and two of A
   __shared__ u32x4 stage[S][8 * 128];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
   const int row0 = blockIdx.x * 64, C = a.slices * a.rank;
@@ -340,8 +355,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a, int 
       if (u0 + i < u1) issue(u0 + i);
     for (int u = u0; u < u1; ++u) {
       // stage u is there for all, and stage u - 1 has been read by all
-      if (u + 2 < u1) barrier_behind<2 * LOADS>();
-      else if (u + 1 < u1) barrier_behind<LOADS>();
+      if (u + 1 < u1) barrier_behind<LOADS>();
       else barrier_behind<0>();
       if (u + S - 1 < u1) issue(u + S - 1);
       const u32x4* from = stage[(u - u0) % S];

@@ -71,11 +71,12 @@ def wq_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residu
         y_at, ld_y = _rows(out, "out", dtype, shape, dev)
     _check_cuda(x, "x")
     at = _stream(stream, dev)
+    plain = stream is None and x.is_contiguous()  # (a little cheaper than _empty)
     if out is None:
-        out = _empty(stream, x, shape)
+        out = torch.empty_like(x) if plain else _empty(stream, x, shape)
         y_at, ld_y = out.data_ptr(), heads * dim
     if residual is not None and sum_out is None:
-        sum_out = _empty(stream, x, shape)
+        sum_out = torch.empty_like(x) if plain else _empty(stream, x, shape)
         s_at, ld_s = sum_out.data_ptr(), heads * dim
     rc = lib().wq_rms_norm(x_at, ld_x, r_at, ld_r, weight.data_ptr(), eps, dt, y_at, ld_y, s_at, ld_s, rows, heads,
                            dim, at)
