@@ -572,7 +572,7 @@ __global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const
       for (int q = 0; q < 4; ++q) {
         const uint32_t o = base + 8 * c < end ? yo[q] : kOutOfRange;
         if constexpr (FEW) yv[q][0] = __builtin_amdgcn_raw_buffer_load_b32(yr, o, (uint32_t)base * 2, 0);
-        else yv[q] = load16(yr, o, (uint32_t)base * 2);
+        else yv[q] = __builtin_amdgcn_raw_buffer_load_b128(yr, o, (uint32_t)base * 2, kNontemporal);  // (read once)
       }
     };
     load(base0);
