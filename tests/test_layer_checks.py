@@ -125,7 +125,7 @@ def test_rotary_refusals(L):
 
 
 def lora_call(L, x=1 << 20, dt=0, a=2 << 20, b=3 << 20, scales=64, ranks=None, ids=64, cu=None, y=4 << 20, out=5 << 20,
-              rows=4, batch=2, num=2, N=512, K=256, rank=16, slices=1, ends=ends_of(512), ws=6 << 20, ws_bytes=1 << 16):
+              rows=100, batch=2, num=2, N=512, K=256, rank=16, slices=1, ends=ends_of(512), ws=6 << 20, ws_bytes=1 << 16):
     return L.wq_lora(P(x), dt, P(a), P(b), P(scales), P(ranks), P(ids), P(cu), P(y), P(out), rows, batch, num, N, K, rank,
                      slices, ends, P(ws), ws_bytes, None)
 
@@ -161,8 +161,11 @@ def test_lora_refusals(L):
     assert lora_call(L, ws_bytes=8) == 4
     assert lora_call(L, ws=(6 << 20) + 8) == 2
     assert lora_call(L, ws=5 << 20) == 1
-    need = wq.wq_lora_workspace_bytes(4, 2, 256, 16)
-    assert need >= 4 * 16 * 4 and lora_call(L, ws_bytes=need - 1) == 4
+    need = wq.wq_lora_workspace_bytes(100, 2, 256, 16)
+    assert need >= 100 * 16 * 4 and lora_call(L, ws_bytes=need - 1) == 4
+    # a few rows of a small adapter need none (an output that overlaps is looked at before)
+    assert wq.wq_lora_workspace_bytes(4, 2, 256, 16) == 0
+    assert lora_call(L, rows=4, ws=None, ws_bytes=0, out=1 << 20) == 1
     for bad in ((0, 1, 256, 16, 1), (4, 2, 200, 16, 1), (4, 2, 256, 20, 1), (4, 2, 256, 16, 5), (4, 0, 256, 16, 1)):
         assert wq.wq_lora_workspace_bytes(*bad) == 0, bad
 
@@ -288,7 +291,7 @@ def test_binding_refuses_before_the_library(L):
     assert "out[1]" in refused(wq.wq_rotary, q, None, plan, kv_lens=lens, out=(q, k))
     assert "rows" in refused(wq.wq_rotary, q[:3], k[:3], plan, kv_lens=lens)
     bank = wq.LoraBank(torch.zeros(2, 16, 256).half(), torch.zeros(2, 64, 16).half(), torch.ones(2))
-    x, y, ids = torch.zeros(4, 256).half(), torch.zeros(4, 64).half(), torch.zeros(2, dtype=torch.int32)
+    x, y, ids = torch.zeros(100, 256).half(), torch.zeros(100, 64).half(), torch.zeros(2, dtype=torch.int32)
     assert "GPU" in refused(wq.wq_lora, x, bank, ids, y)
     assert "K" in refused(wq.wq_lora, x[:, :128], bank, ids, y)
     assert "bank" in refused(wq.wq_lora, x.bfloat16(), bank, ids, y.bfloat16())

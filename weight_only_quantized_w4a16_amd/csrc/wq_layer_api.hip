@@ -189,8 +189,8 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
       bytes_meet(a, na, out, ny) || bytes_meet(b, nb, out, ny))
     return WQ_EINVAL;
   const size_t need = lora_workspace_bytes(rows, batch, K, rank, slices);
-  if (!ws || ws_bytes < need) return WQ_ENOSPACE;
-  if ((uintptr_t)ws & 15) return WQ_EUNSUPPORTED;
+  if (need && (!ws || ws_bytes < need)) return WQ_ENOSPACE;
+  if (need && ((uintptr_t)ws & 15)) return WQ_EUNSUPPORTED;
   if (bytes_meet(ws, need, out, ny) || bytes_meet(ws, need, x, (size_t)rows * K * 2) || bytes_meet(ws, need, y, ny))
     return WQ_EINVAL;
   r.x = (const uint16_t*)x;

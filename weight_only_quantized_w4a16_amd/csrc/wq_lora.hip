@@ -15,11 +15,11 @@
 //
 // What bounds them (MI355X, graph-replayed, banks and rows from memory).  Few rows:
 // launches and the chain offsets -> adapter -> rank -> data; one row of rank 16
-// over 4096 x 4096 takes 7.6 us for 0.3 MB, 64 tokens of 40 adapters of ranks 8
-// to 32 beside 8192 -> 10240 20.5 us for 52 MB (first product 10.8 us at 3.3
+// beside 4096 -> 4096 takes 6.3 us for 0.3 MB, 64 tokens of 40 adapters of ranks 8
+// to 32 beside 8192 -> 10240 20.8 us for 52 MB (first product 10.8 us at 3.3
 // TB/s, second 9.2).  Many: 6400 prompt rows of rank 64 beside 4096 -> 12288 take
-// 117 us: 34 us for x A^T (LDS and the latency of its stages), 6 to put its parts
-// together, 76 us for the 315 MB of y and out (4.1 TB/s; a copy: 4.75).
+// 113 us: 30 us for x A^T (LDS and the latency of its stages), 6 to put its parts
+// together, 75 us for the 315 MB of y and out (4.2 TB/s; a copy: 4.75).
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -64,6 +64,17 @@ LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0) {
   const int64_t blocks = (int64_t)((N + 127) / 128) * tiles * p.groups / 1280;
   p.blocks = blocks < 1 ? 1 : blocks > 8 ? 8 : (int)blocks;
   return p;
+}
+
+// One launch, for calls whose time is launches; every workgroup then reads the slice's A
+// for itself.  Captured, two launches : one, us, beside 4096 -> 4096 (or 3 x 4096): one
+// row of rank 16 7.3 : 6.3 (7.4 : 6.4), of rank 32 7.4 : 8.3, of 11008 -> 4096 8.6 : 8.5;
+// 16 rows of one adapter of rank 16 8.1 : 7.9, of many (11.5 : 11.6) to (14.4 : 11.8), of
+// rank 8 from 11008 9.4 : 11.3; 64 rows of one 10.1 : 11.6.  Not captured, the launch
+// and the workspace it saves are 3.5 us of host time.
+bool lora_fused(int rows, int K, int rank) {
+  if (rank > 32) return false;
+  return rows <= 4 && rank <= 16 ? rank * K <= 180224 : rows <= 16 && rank * K <= 65536;
 }
 
 __device__ inline u32x4 load16(rsrc_t r, uint32_t voff, uint32_t soff) {
@@ -631,6 +642,184 @@ __global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const
   });
 }
 
+// Both products in one launch, for calls whose time is launches.  A workgroup takes up to
+// four rows of one adapter and `blocks` pairs of 128 columns of one slice: its eight waves
+// form the slice's v themselves (row by row, as lora_shrink_rows_kernel does; every
+// workgroup of the slice reads A again, from the caches), add it up in LDS, and multiply B
+// by it, four waves to a block of columns (as lora_expand_kernel's few rows do).
+template <int DT>
+__global__ __launch_bounds__(512) void lora_fused_kernel(const LoraArgs a, int blocks) {
+  constexpr int KC = 1, NL = 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
+  const int half = wave >> 2, part = wave & 3, t256 = threadIdx.x & 255;
+  const int row0 = blockIdx.x * 64, C = a.slices * a.rank, R8 = a.rank >> 3, magic = (65535 + R8) / R8;
+  int slice = 0, first = 0, end = a.ends[0], chunk = blockIdx.y;
+  for (;;) {
+    const int n = (end - first + 256 * blocks - 1) / (256 * blocks);
+    if (chunk < n) break;
+    chunk -= n;
+    first = end;
+    end = a.ends[++slice];
+  }
+  const int base0 = first + chunk * blocks * 256, stop = base0 + blocks * 256 < end ? base0 + blocks * 256 : end;
+  const int ids = tile_adapters<64>(a, row0, lane);
+  const int left = a.seqs.rows - row0, tile_rows = __builtin_amdgcn_readfirstlane(left < 64 ? left : 64);
+  const rsrc_t xr = make_rsrc(a.x + (int64_t)row0 * a.K, (uint32_t)tile_rows * a.K * 2);
+  const rsrc_t yr = make_rsrc(a.y + (int64_t)row0 * a.N, (uint32_t)tile_rows * a.N * 2);
+  const rsrc_t outr = make_rsrc(a.out + (int64_t)row0 * a.N, (uint32_t)tile_rows * a.N * 2);
+  const int units = a.K / 128;
+  const int k0 = units * wave / 8 * 128, k1 = units * (wave + 1) / 8 * 128;
+  __shared__ u32x4 stage[2][2][512 * KC];
+  __shared__ f4 red[8][4][32 * KC / 4];  // [wave][row of x][row of A]
+  int buf = 0;
+
+  each_adapter<4>(ids, a.y == a.out ? 0 : -1, blockIdx.z, gridDim.z, [&](int cur, int before) {
+    const int rank = cur < 0 ? 0 : adapter_rank(a, cur);
+    const float scale = cur < 0 ? 0.f : a.scales[cur];
+    const rsrc_t ar = make_rsrc(a.a + (int64_t)(cur < 0 ? 0 : cur) * C * a.K, (uint32_t)C * a.K * 2);
+    const rsrc_t br = make_rsrc(a.b + (int64_t)(cur < 0 ? 0 : cur) * a.N * a.rank, (uint32_t)a.N * a.rank * 2);
+    uint64_t mask = __ballot(ids == cur);
+    for (int i = 0; i < before; ++i) mask &= mask - 1;
+    int row[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      row[t] = mask ? __builtin_ctzll(mask) : -1;
+      mask &= mask - 1;
+    }
+    // B and y of the first columns, needed last
+    uint32_t bo[NL], yo[4];
+    int bn[NL];  // column of the chunk this thread loads
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+      const int at = l * 256 + t256, s = at ^ (((at >> 3) * magic >> 16) & 7), n = s * magic >> 16;
+      const bool ok = at < 128 * R8 && 8 * (s - n * R8) < rank;
+      bo[l] = (uint32_t)s * 16;
+      bn[l] = ok ? n : 1 << 24;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)  // (the results' rows 4 h + q are rows of x for h = 0)
+      yo[q] = h == 0 && row[q] >= 0 ? ((uint32_t)row[q] * a.N + 8 * c + 2 * part) * 2 : kOutOfRange;
+    u32x4 bv[NL];
+    uint32_t yv[4];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+        bv[l] = load16(br, base + bn[l] < end ? bo[l] : kOutOfRange, (uint32_t)base * a.rank * 2);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        yv[q] = __builtin_amdgcn_raw_buffer_load_b32(yr, base + 8 * c < end ? yo[q] : kOutOfRange, (uint32_t)base * 2, 0);
+    };
+    load(base0 + 128 * half);
+    // v of this slice, 16 rows of A at a time
+    auto product = [&](auto tg) {
+      constexpr int TG = decltype(tg)::value, D = TG == 1 ? 4 : 2;
+      uint32_t xo[TG];
+#pragma unroll
+      for (int t = 0; t < TG; ++t) xo[t] = row[t] >= 0 ? ((uint32_t)row[t] * a.K + 8 * c) * 2 : kOutOfRange;
+      for (int b = 0; 16 * b < rank; ++b) {
+        uint32_t ao[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = 16 * b + 4 * r + h;
+          ao[r] = j < rank ? ((uint32_t)(slice * a.rank + j) * a.K + 8 * c) * 2 : kOutOfRange;
+        }
+        f4 acc[4][TG] = {};
+        u32x4 af[D][4], xf[D][TG];
+        auto fetch = [&](int u, int k) {
+          const uint32_t out = k < k1 ? 0u : kOutOfRange;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) af[u][r] = load16(ar, ao[r] | out, k * 2);
+#pragma unroll
+          for (int t = 0; t < TG; ++t) xf[u][t] = load16(xr, xo[t] | out, k * 2);
+        };
+#pragma unroll
+        for (int u = 0; u < D - 1; ++u) fetch(u, k0 + 128 * u);
+        for (int k = k0; k < k1; k += 128 * D)  // (what lies past the range comes as zeros)
+#pragma unroll
+          for (int u = 0; u < D; ++u) {
+            fetch((u + D - 1) % D, k + 128 * (u + D - 1));
+#pragma unroll
+            for (int q = 0; q < 4; q += 2)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+                  acc[r][t] = mfma4<DT>(af[u][r][q], af[u][r][q + 1], xf[u][t][q], xf[u][t][q + 1], acc[r][t]);
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int t = 0; t < TG; ++t) {
+            const f4 v = acc[r][t];
+            const float own = lane & 2 ? (lane & 1 ? v[3] : v[2]) : (lane & 1 ? v[1] : v[0]);
+            float s = sum_row(own);
+            if (16 * b + 4 * r + h >= rank) s = 0.f;  // (0 x is not 0 for every x)
+            if (c == 0) ((float*)red[wave][t])[16 * b + 4 * r + h] = s;
+          }
+      }
+    };
+    if (row[1] >= 0) product(std::integral_constant<int, 4>{});
+    else product(std::integral_constant<int, 1>{});
+    __syncthreads();
+    u32x4 hi[KC], lo[KC], keep[KC];
+    f4 v[KC][2] = {};
+    const bool own = c == 0 || (c < 4 && row[1] >= 0);  // (with one row the others' sums are not there)
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (own && 32 * k + 8 * h + 4 * i < rank)
+#pragma unroll
+          for (int w = 0; w < 8; ++w) v[k][i] += red[w][c & 3][8 * k + 2 * h + i];
+    float up = 1.f, down = 1.f;
+    if constexpr (DT == F16) {
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) m = fmaxf(m, largest(v[k][0], v[k][1]));
+      m = fmaxf(m, __shfl_xor(m, 16, 64));
+      m = fmaxf(m, __shfl_xor(m, 32, 64));
+      powers(m, up, down);
+    }
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      two_parts<DT>(v[k][0], v[k][1], up, hi[k], lo[k]);
+      const int n = rank - 32 * k - 8 * h;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) keep[k][q] = n <= 2 * q ? 0u : n == 2 * q + 1 ? 0xFFFFu : 0xFFFFFFFFu;
+    }
+    down *= scale;
+    float back[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) back[q] = __shfl(down, q, 64);
+    for (int at = base0; at < stop; at += 256, buf ^= 1) {  // (both halves go round as often)
+      const int base = at + 128 * half;
+      uint32_t yc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) yc[q] = yv[q];
+#pragma unroll
+      for (int l = 0; l < NL; ++l) stage[buf][half][l * 256 + t256] = bv[l];
+      if (at + 256 < stop) load(base + 256);
+      __syncthreads();  // (the block before the last one has been read by all, and red by all)
+      f4 d[2] = {};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          const u32x4 bt = stage[buf][half][((8 * c + t + 2 * part) * R8 + 4 * k + h) ^ (c & 7)] & keep[k];
+          d[t] = mfma16<DT>(lo[k], bt, d[t]);
+          d[t] = mfma16<DT>(hi[k], bt, d[t]);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o = pack2<DT>(__builtin_fmaf(d[0][q], back[q], act_lo<DT>(yc[q])),
+                               __builtin_fmaf(d[1][q], back[q], act_hi<DT>(yc[q])));
+        if (rank == 0) o = yc[q];  // (no adapter: a copy)
+        __builtin_amdgcn_raw_buffer_store_b32(o, outr, (base + 8 * c < end ? yo[q] : kOutOfRange) + (uint32_t)base * 2, 0, 0);
+      }
+    }
+  });
+}
+
 template <int DT, bool FEW, int KC>
 void expand(const LoraArgs& a, const LoraPlan& p, int tiles, hipStream_t s) {
   int chunks = 0;
@@ -642,6 +831,16 @@ void expand(const LoraArgs& a, const LoraPlan& p, int tiles, hipStream_t s) {
 template <int DT>
 wq_status launch(const LoraArgs& a, hipStream_t s) {
   const int columns = a.slices * a.rank;
+  if (lora_fused(a.seqs.rows, a.K, a.rank)) {
+    const int groups = a.seqs.batch < 64 ? a.seqs.batch : 64;
+    int blocks = (a.N + 255) / 256 * groups / 128;  // (128 workgroups: 16 rows of 16 adapters 11.8 us, 256 18.7)
+    blocks = blocks < 1 ? 1 : blocks > 16 ? 16 : blocks;
+    int chunks = 0;
+    for (int i = 0; i < a.slices; ++i) chunks += (a.ends[i] - (i ? a.ends[i - 1] : 0) + 256 * blocks - 1) / (256 * blocks);
+    const dim3 grid((a.seqs.rows + 63) / 64, chunks, groups), block(512);
+    hipLaunchKernelGGL((lora_fused_kernel<DT>), grid, block, 0, s, a, blocks);
+    return launch_status();
+  }
   const LoraPlan p = lora_plan(a.seqs.rows, a.seqs.batch, a.K, columns, a.N);
   const int tiles = (a.seqs.rows + 63) / 64, kc = (a.rank + 31) / 32;
   const int width = p.few ? 16 : 64;
@@ -666,6 +865,7 @@ wq_status launch(const LoraArgs& a, hipStream_t s) {
 // Parts of v; for many rows then its two 16-bit parts and the powers of two.
 static size_t part_bytes(const LoraPlan& p, int rows, int columns) { return (size_t)p.splits * rows * columns * 4; }
 size_t lora_workspace_bytes(int rows, int batch, int K, int rank, int slices) {
+  if (lora_fused(rows, K, rank)) return 0;
   const LoraPlan p = lora_plan(rows, batch, K, rank * slices);
   return part_bytes(p, rows, rank * slices) + (p.few ? 0 : (size_t)rows * slices * (4 * rank + 4));
 }
