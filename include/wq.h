@@ -441,7 +441,7 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
  *   ws       : wq_lora_workspace_bytes() bytes for these sizes, 16-byte aligned (may be
  *              NULL when 0); calls that overlap in time must not share it
  * All pointers but adapters, scales, ranks and cu_q are 16-byte aligned.  K % 128 == 0,
- * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24 (else
+ * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24, rows N <= 2^38 (else
  * WQ_EUNSUPPORTED).
  * Rows outside every sequence are left as they were.  fp32 accumulation; x A^T enters
  * the second product in two parts that hold it to 2^-16 (bf16) or 2^-22 (fp16) of the

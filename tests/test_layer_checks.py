@@ -149,6 +149,7 @@ def test_lora_refusals(L):
     assert lora_call(L, rows=3) == 1
     assert lora_call(L, batch=0) == 1
     assert lora_call(L, rows=1 << 25, batch=1) == 2
+    assert lora_call(L, rows=1 << 24, batch=1, N=1 << 20, ends=ends_of(1 << 20)) == 2
     for name in ("x", "a", "b", "scales", "ids", "y", "out"):
         assert lora_call(L, **{name: None}) == 1, name
     for name in ("x", "a", "b", "y", "out"):
@@ -160,7 +161,9 @@ def test_lora_refusals(L):
     assert lora_call(L, ws=None) == 4
     assert lora_call(L, ws_bytes=8) == 4
     assert lora_call(L, ws=(6 << 20) + 8) == 2
-    assert lora_call(L, ws=5 << 20) == 1
+    assert lora_call(L, ws=5 << 20) == 1                      # over out, a, b
+    assert lora_call(L, ws=2 << 20) == 1
+    assert lora_call(L, ws=3 << 20) == 1
     need = wq.wq_lora_workspace_bytes(100, 2, 256, 16)
     assert need >= 100 * 16 * 4 and lora_call(L, ws_bytes=need - 1) == 4
     # a few rows of a small adapter need none (an output that overlaps is looked at before)

@@ -181,6 +181,7 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
   wq_status st = make_seqs(r.seqs, nullptr, cu_q, rows, batch);
   if (st != WQ_OK) return st;
   if (rows == 0) return WQ_OK;
+  if ((int64_t)rows * N > (int64_t)1 << 38) return WQ_EUNSUPPORTED;  // (more than a GPU holds, and than one grid)
   if (!x || !a || !b || !scales || !adapters || !y || !out) return WQ_EINVAL;
   if (((uintptr_t)x | (uintptr_t)a | (uintptr_t)b | (uintptr_t)y | (uintptr_t)out) & 15) return WQ_EUNSUPPORTED;
   const size_t ny = (size_t)rows * N * 2;
@@ -191,7 +192,8 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
   const size_t need = lora_workspace_bytes(rows, batch, K, rank, slices);
   if (need && (!ws || ws_bytes < need)) return WQ_ENOSPACE;
   if (need && ((uintptr_t)ws & 15)) return WQ_EUNSUPPORTED;
-  if (bytes_meet(ws, need, out, ny) || bytes_meet(ws, need, x, (size_t)rows * K * 2) || bytes_meet(ws, need, y, ny))
+  if (bytes_meet(ws, need, out, ny) || bytes_meet(ws, need, x, (size_t)rows * K * 2) || bytes_meet(ws, need, y, ny) ||
+      bytes_meet(ws, need, a, na) || bytes_meet(ws, need, b, nb))
     return WQ_EINVAL;
   r.x = (const uint16_t*)x;
   r.a = (const uint16_t*)a;

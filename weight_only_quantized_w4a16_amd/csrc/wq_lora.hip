@@ -18,8 +18,8 @@
 // beside 4096 -> 4096 takes 6.3 us for 0.3 MB, 64 tokens of 40 adapters of ranks 8
 // to 32 beside 8192 -> 10240 20.8 us for 52 MB (first product 10.8 us at 3.3
 // TB/s, second 9.2).  Many: 6400 prompt rows of rank 64 beside 4096 -> 12288 take
-// 113 us: 30 us for x A^T (LDS and the latency of its stages), 6 to put its parts
-// together, 75 us for the 315 MB of y and out (4.2 TB/s; a copy: 4.75).
+// 101 us: 30 us for x A^T (LDS and the latency of its stages), 6 to put its parts
+// together, 63 us for the 315 MB of y and out (5.0 TB/s, y partly from the caches; a copy: 4.75).
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -59,10 +59,13 @@ LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0) {
       }
     }
   }
-  // about 1280 workgroups (64 tokens of 40 adapters: 20.2 us, 21.6 with 640, 25.9 with
-  // 2048; prompts 117, 120 with 768, 118 with 2048)
+  // 1280 to 2560 workgroups (64 tokens of 40 adapters: 20.2 us, 21.6 with 640, 25.9 with
+  // 3840), each with a power of two of column blocks: a tile's workgroups are then mostly a
+  // multiple of the eight XCDs, whose caches so keep the same columns' B (the prompts'
+  // second product 63.4 us with 24 workgroups a tile; 70.6 with 15, 68 with 18 or 21, 67.3
+  // with 33)
   const int64_t blocks = (int64_t)((N + 127) / 128) * tiles * p.groups / 1280;
-  p.blocks = blocks < 1 ? 1 : blocks > 8 ? 8 : (int)blocks;
+  p.blocks = blocks < 2 ? 1 : blocks < 4 ? 2 : blocks < 8 ? 4 : 8;
   return p;
 }
 
@@ -505,19 +508,21 @@ __global__ __launch_bounds__(256) void lora_split_kernel(const LoraArgs a, int s
 
 // out = y + scale v B^T; KC: blocks of 32 of the rank.  A workgroup takes 64 rows and
 // `blocks` blocks of 128 columns of one slice.  B goes through LDS: consecutive threads
-// load consecutive 16 bytes of it (chunk s of a block lies at s ^ (s / rank % 8), which
-// spreads the operands over the banks), and column 8 j + t is column j of tile t, so that
+// load consecutive 16 bytes of it (chunk s of a block, which belongs to column s / R8, R8 to
+// a column, lies at s ^ (s / 8 R8 % 16), % 8 with odd R8: that spreads the operands over
+// the banks), and column 8 j + t is column j of tile t, so that
 // the results of the eight tiles are eight consecutive columns of four rows in a lane:
 // y is read and out written 256 consecutive bytes at a time.  (With 64 bytes of sixteen
-// rows a load, B straight from memory: 91 us instead of 76 for the prompts.)  Many rows:
+// rows a load, B straight from memory: 91 us instead of 75 for the prompts.)  Many rows:
 // a wave to 16 of them, all eight tiles.  Few: the waves share up to 16 rows of an
 // adapter and take two tiles each.
 template <int DT, bool FEW, int KC>
-__global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const LoraArgs a, int splits, int blocks) {
+__global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const LoraArgs a, int splits, int blocks, uint32_t chunks) {
   constexpr int NT = FEW ? 2 : 8, NL = 2 * KC;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
-  const int row0 = blockIdx.x * 64, R8 = a.rank >> 3, magic = (65535 + R8) / R8;  // x / R8 = x magic >> 16, x < 2048
-  int slice = 0, first = 0, end = a.ends[0], chunk = blockIdx.y;
+  const int row0 = (int)(blockIdx.x / chunks) * 64, R8 = a.rank >> 3, magic = (65535 + R8) / R8;  // x / R8 = x magic >> 16, x < 2048
+  const int spread = R8 & 1 ? 7 : 15;
+  int slice = 0, first = 0, end = a.ends[0], chunk = (int)(blockIdx.x % chunks);
   for (;;) {
     const int n = (end - first + 128 * blocks - 1) / (128 * blocks);
     if (chunk < n) break;
@@ -541,7 +546,7 @@ __global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const
     int bn[NL];  // column of the chunk this thread loads
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      const int at = l * 256 + threadIdx.x, s = at ^ (((at >> 3) * magic >> 16) & 7), n = s * magic >> 16;
+      const int at = l * 256 + threadIdx.x, s = at ^ (((at >> 3) * magic >> 16) & spread), n = s * magic >> 16;
       const bool ok = at < 128 * R8 && 8 * (s - n * R8) < rank;
       bo[l] = (uint32_t)s * 16;
       bn[l] = ok ? n : 1 << 24;
@@ -621,7 +626,7 @@ __global__ __launch_bounds__(256, KC == 4 ? 2 : 3) void lora_expand_kernel(const
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
-          const u32x4 bt = stage[buf][((8 * c + t + (FEW ? 2 * wave : 0)) * R8 + 4 * k + h) ^ (c & 7)] & keep[k];
+          const u32x4 bt = stage[buf][((8 * c + t + (FEW ? 2 * wave : 0)) * R8 + 4 * k + h) ^ (c & spread)] & keep[k];
           d[t] = mfma16<DT>(lo[k], bt, d[t]);
           d[t] = mfma16<DT>(hi[k], bt, d[t]);
         }
@@ -653,6 +658,7 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const LoraArgs a, int b
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15, h = lane >> 4;
   const int half = wave >> 2, part = wave & 3, t256 = threadIdx.x & 255;
   const int row0 = blockIdx.x * 64, C = a.slices * a.rank, R8 = a.rank >> 3, magic = (65535 + R8) / R8;
+  const int spread = R8 & 1 ? 7 : 15;
   int slice = 0, first = 0, end = a.ends[0], chunk = blockIdx.y;
   for (;;) {
     const int n = (end - first + 256 * blocks - 1) / (256 * blocks);
@@ -691,7 +697,7 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const LoraArgs a, int b
     int bn[NL];  // column of the chunk this thread loads
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      const int at = l * 256 + t256, s = at ^ (((at >> 3) * magic >> 16) & 7), n = s * magic >> 16;
+      const int at = l * 256 + t256, s = at ^ (((at >> 3) * magic >> 16) & spread), n = s * magic >> 16;
       const bool ok = at < 128 * R8 && 8 * (s - n * R8) < rank;
       bo[l] = (uint32_t)s * 16;
       bn[l] = ok ? n : 1 << 24;
@@ -805,7 +811,7 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const LoraArgs a, int b
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
-          const u32x4 bt = stage[buf][half][((8 * c + t + 2 * part) * R8 + 4 * k + h) ^ (c & 7)] & keep[k];
+          const u32x4 bt = stage[buf][half][((8 * c + t + 2 * part) * R8 + 4 * k + h) ^ (c & spread)] & keep[k];
           d[t] = mfma16<DT>(lo[k], bt, d[t]);
           d[t] = mfma16<DT>(hi[k], bt, d[t]);
         }
@@ -825,7 +831,10 @@ void expand(const LoraArgs& a, const LoraPlan& p, int tiles, hipStream_t s) {
   int chunks = 0;
   for (int i = 0; i < a.slices; ++i)
     chunks += (a.ends[i] - (i ? a.ends[i - 1] : 0) + 128 * p.blocks - 1) / (128 * p.blocks);
-  hipLaunchKernelGGL((lora_expand_kernel<DT, FEW, KC>), dim3(tiles, chunks, p.groups), dim3(256), 0, s, a, p.splits, p.blocks);
+  // (a tile's workgroups lie next to each other, so that whole rows of y are read and
+  // written at a time: 70.6 us for the prompts, 75 with a column's next to each other)
+  hipLaunchKernelGGL((lora_expand_kernel<DT, FEW, KC>), dim3((uint32_t)tiles * chunks, 1, p.groups), dim3(256), 0, s, a,
+                     p.splits, p.blocks, (uint32_t)chunks);
 }
 
 template <int DT>
