@@ -207,6 +207,8 @@ def test_refusals(wq, model):
         CachedStack(*args, adapters=banks).step(x, i32([[0]]), i32([1]))
     with pytest.raises(ValueError, match="adapter"):
         CachedStack(*args).step(x, i32([[0]]), i32([1]), adapters=i32([0]))
+    with pytest.raises(ValueError, match="2 sequences need as many adapters"):
+        CachedStack(*args, adapters=banks).step(x.repeat(2, 1), i32([[0], [1]]), i32([1, 1]), adapters=i32([0]))
     with pytest.raises(ValueError, match="positions"):
         CachedStack(*args).step(x, i32([[0]]), i32([1]), positions=i32([0]))
     # a product without adapters among those that have them

@@ -288,6 +288,7 @@ def test_binding_refuses_before_the_library(L):
     assert "kv_lens" in refused(wq.wq_rotary, q, k, plan)
     assert "either" in refused(wq.wq_rotary, q, k, plan, positions=torch.zeros(4, dtype=torch.int32), kv_lens=lens)
     assert "positions" in refused(wq.wq_rotary, q, k, plan, positions=torch.zeros(4))
+    assert "positions" in refused(wq.wq_rotary, q, k, plan, positions=[0, 1, 2, 3])
     assert "positions" in refused(wq.wq_rotary, q, k, plan, positions=torch.zeros(2, 4, dtype=torch.int32))
     assert "k must" in refused(wq.wq_rotary, q, k[:3], plan, kv_lens=lens)
     assert "channels" in refused(wq.wq_rotary, torch.zeros(4, 8, 32).half(), k, plan, kv_lens=lens)

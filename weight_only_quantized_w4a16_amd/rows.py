@@ -178,6 +178,7 @@ def wq_rotary(q: torch.Tensor, k: Optional[torch.Tensor], plan: Rotary, position
     ld_pos = batch = 0
     if positions is not None:
         _need(kv_lens is None and cu_q is None, "either positions or kv_lens")
+        _need(isinstance(positions, torch.Tensor), "positions must be a tensor")
         _check_tensor(positions, "positions", (torch.int32,), (rows,) if positions.dim() == 1 else (plan.num_axes, rows),
                       dev)
         ld_pos = rows if positions.dim() == 2 else 0

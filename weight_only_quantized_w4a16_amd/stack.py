@@ -202,6 +202,8 @@ class CachedStack:
         ws = _empty(stream, x, need, torch.uint8, scratch=True) if need else None
         if (self.adapters is None) != (adapters is None):
             raise ValueError("a stack with adapters, and no other, needs each sequence's adapter")
+        if adapters is not None and adapters.shape != kv_lens.shape:
+            raise ValueError(f"{kv_lens.shape[0]} sequences need as many adapters, got {tuple(adapters.shape)}")
         if positions is not None and self.rotary is None:
             raise ValueError("positions are for a stack with rotary positions")
         lora_ws = None
