@@ -186,11 +186,11 @@ __device__ inline float sum_row(float v) {
 }
 
 // v = x A^T for few rows: 16 rows of A for the rows of x that share the adapter, up to
-// four of them to a workgroup.  The work is to read A: consecutive lanes take consecutive 16 bytes (a
-// load is 256 bytes of four rows), every lane multiplies its entries of A and x, and the
-// lanes are added up at the end.  (As operands of the 16-row product a load would be 64
-// bytes of sixteen rows at a stride of 16 lanes: 18.2 us instead of 10.8 for 64 tokens of
-// 40 adapters.)  The four waves (and the parts) split K.
+// four of them to a workgroup.  The work is to read A: consecutive lanes take consecutive
+// 16 bytes (a load is 256 bytes of four rows), every lane multiplies its entries of A and
+// x, and the lanes are added up at the end.  (As operands of the 16-row product a load
+// would be 64 bytes of sixteen rows at a stride of 16 lanes: 18.2 us instead of 10.8 for
+// 64 tokens of 40 adapters.)  The four waves (and the parts) split K.
 template <int DT>
 __global__ __launch_bounds__(256, 3) void lora_shrink_rows_kernel(const LoraArgs a, int splits) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -318,10 +318,10 @@ __device__ inline void barrier_behind() {
 // v = x A^T for many rows: 64 rows of x and 64 of A, 64 of K at a time, in a ring of
 // three stages in LDS that LDS-destination loads fill, two of them in flight (two stages
 // 32 us, three 31, four 34 for 6400 rows of 192 columns: three leave room for three
-// workgroups on a CU).  A load takes
-// 128 consecutive bytes of eight rows by consecutive lanes (operands loaded straight
-// into registers, 64 bytes of sixteen rows at a stride of 16 lanes, took 55 us); 16-byte chunk j of a row lies at j ^ (row % 8), so that the operands are read without
-// bank conflicts.  A wave multiplies all the rows by 16 of A.
+// workgroups on a CU).  A load takes 128 consecutive bytes of eight rows by consecutive
+// lanes (operands loaded straight into registers, 64 bytes of sixteen rows at a stride of
+// 16 lanes, took 55 us); 16-byte chunk j of a row lies at j ^ (row % 8), so that the
+// operands are read without bank conflicts.  A wave multiplies all the rows by 16 of A.
 template <int DT>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a, int splits) {
   constexpr int S = 3, LOADS = 4;  // stages; loads of a wave for one, two of x and two of A
