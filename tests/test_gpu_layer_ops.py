@@ -375,6 +375,41 @@ def test_resize_takes_what_comes_back():
     assert wq.wq_kv_resize(empty, i32([]), 2)[0].tolist() == [0] and empty.counts.tolist() == [4, 0]
 
 
+@pytest.mark.parametrize("batch", [3, 1024, 1025])
+def test_resize_of_many_rows(batch):
+    """More rows than one workgroup takes: changes that fit, that lack pages and that have no place, eager and captured."""
+    per = 24000 // batch
+    cap = -(-per // 16) + 2
+    num_pages = batch * (cap - 1)
+    pages = wq.wq_kv_pages(num_pages, 16, batch, cap)
+    ref = _layer.Pages([[-1] * cap for _ in range(batch)], [0] * batch, range(num_pages - 1, -1, -1), num_pages, 16)
+    even, odd = [per if b % 2 == 0 else 0 for b in range(batch)], [per if b % 2 else 0 for b in range(batch)]
+    changes = [even, [per + 16] * batch, odd, [per] * (batch - 1) + [16 * cap + 1], [16 * cap] * batch, even[::-1],
+               [n - n % 5 for n in odd], [0] * batch]
+    assert batch * cap > num_pages and sum(even) > 8192 and sum(odd) > 7000
+    lacked = []
+    for want in changes:
+        expect = ref.resize(want, 20000)
+        lacked.append(ref.lack)
+        same(pages, ref, wq.wq_kv_resize(pages, i32(want), 20000), expect)
+    assert lacked[3] == -1 and lacked[4] > 0 and lacked.count(0) == len(changes) - 2
+    want = i32(changes[0])
+    wq.wq_kv_resize(pages, want, 20000)  # (and back: the state that the graph is captured from)
+    wq.wq_kv_resize(pages, i32([0] * batch))
+    main = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        out = wq.wq_kv_resize(pages, want, 20000)
+    ref.resize(changes[0], 20000), ref.resize(changes[-1], 0)
+    for wanted in changes:
+        want.copy_(i32(wanted))
+        expect = ref.resize(wanted, 20000)
+        graph.replay()
+        torch.cuda.synchronize()
+        same(pages, ref, out, expect)
+
+
 # ---------------------------------------------------------------------------- streams and graphs
 def test_calls_on_another_stream_and_in_a_graph():
     """Each operator on an explicit stream, and captured: every replay gives the eager results on new inputs."""

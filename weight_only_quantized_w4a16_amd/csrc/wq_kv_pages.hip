@@ -14,8 +14,10 @@
 // entries given back those behind its last.
 //
 // A step of few sequences and rows is one workgroup, its sums in LDS: the time is
-// a launch and the chain lengths -> sums -> pages -> rows.  Prompts take three
-// launches, one thread to a page and to four rows.
+// a launch and the chain lengths -> sums -> pages -> rows.  Prompts take two
+// launches, one thread to a page and to four rows; every workgroup of the first
+// forms the sums for itself.  Batches whose sums LDS does not hold take three, the
+// sums in one of their own.
 #include "wq_layer.hpp"
 
 namespace wq {
@@ -86,9 +88,22 @@ struct Offsets {
 };
 __device__ inline Offsets offsets_in(int32_t* p, int batch) { return {p, p + (batch + 1), p + 2 * (batch + 1)}; }
 
-// The sums, the verdict, lengths and counts.  `sums` come back as zeros where nothing
-// may change.  Every thread has read what it needs of lens and counts before any writes.
-__device__ inline Sums settle(const PagesArgs& a, const Offsets& o, int64_t& top) {
+// What the sums say; all zeros and the stack as it is where nothing may change.
+struct Verdict {
+  Sums total;
+  int64_t top;
+  int status;
+};
+__device__ inline void set_counts(const PagesArgs& a, int status, int free) {
+  if (status == 0) a.counts[0] = free;
+  a.counts[1] = status;
+}
+
+// The sums and the verdict, for a workgroup of kThreads; with WRITE also lengths, counts
+// and the offsets the caller gets.  (Every thread has read what it needs of lengths and
+// counts before any writes.)
+template <bool WRITE>
+__device__ inline Verdict settle(const PagesArgs& a, const Offsets& o) {
   const int t = threadIdx.x, B = a.batch;
   const int per = (B + kThreads - 1) / kThreads, b0 = t * per < B ? t * per : B, b1 = b0 + per < B ? b0 + per : B;
   Sums own = {0, 0, 0};
@@ -103,33 +118,33 @@ __device__ inline Sums settle(const PagesArgs& a, const Offsets& o, int64_t& top
   Sums at, total;
   sum_before(own, at, total);
   bad = __syncthreads_or(bad);
-  top = count + total.back;
-  int status = 0;
-  if (bad || top > a.num_pages || total.rows > (1 << 24)) status = -1;
-  else if (total.taken > top) status = (int)(total.taken - top);
-  if (status) {
-    total = at = {0, 0, 0};
-    top = count;
+  Verdict v = {total, count + total.back, 0};
+  if (bad || v.top > a.num_pages || total.rows > (1 << 24)) v.status = -1;
+  else if (total.taken > v.top) v.status = (int)(total.taken - v.top);
+  if (v.status) {
+    v.total = at = {0, 0, 0};
+    v.top = count;
   }
   for (int b = b0; b < b1; ++b) {
     o.back[b] = (int)at.back;
     o.taken[b] = (int)at.taken;
     o.rows[b] = (int)at.rows;
-    if (a.cu_q) a.cu_q[b] = (int)at.rows;
-    if (status) continue;
+    if (WRITE && a.cu_q) a.cu_q[b] = (int)at.rows;
+    if (v.status) continue;
     const Lens l = lens_of(a, b);
     at = at + change(a, l);
-    a.lens[b] = l.want;
+    if (WRITE) a.lens[b] = l.want;
   }
   if (t == 0) {
-    o.back[B] = (int)total.back;
-    o.taken[B] = (int)total.taken;
-    o.rows[B] = (int)total.rows;
-    if (a.cu_q) a.cu_q[B] = (int)total.rows;
-    if (status == 0) a.counts[0] = (int)(top - total.taken);
-    a.counts[1] = status;
+    o.back[B] = (int)v.total.back;
+    o.taken[B] = (int)v.total.taken;
+    o.rows[B] = (int)v.total.rows;
+    if (WRITE) {
+      if (a.cu_q) a.cu_q[B] = (int)v.total.rows;
+      set_counts(a, v.status, (int)(v.top - v.total.taken));
+    }
   }
-  return total;
+  return v;
 }
 
 // The f-th page given back and the f-th taken.
@@ -165,11 +180,10 @@ __device__ inline void map_row(const PagesArgs& a, const Offsets& o, int b, int 
 __global__ __launch_bounds__(kThreads) void resize_kernel(const PagesArgs a) {
   __shared__ int32_t sums[3 * (kThreads + 1)];
   const Offsets o = offsets_in(sums, a.batch);
-  int64_t top;
-  const Sums total = settle(a, o, top);
+  const Verdict v = settle<true>(a, o);
   __syncthreads();
-  const int nback = (int)total.back, ntake = (int)total.taken, new_rows = (int)total.rows;
-  for (int f = threadIdx.x; f < (nback > ntake ? nback : ntake); f += kThreads) move_page(a, o, nback, ntake, top, f);
+  const int nback = (int)v.total.back, ntake = (int)v.total.taken, new_rows = (int)v.total.rows;
+  for (int f = threadIdx.x; f < (nback > ntake ? nback : ntake); f += kThreads) move_page(a, o, nback, ntake, v.top, f);
   __syncthreads();
   for (int r = threadIdx.x; r < a.rows; r += kThreads) {
     int pos;
@@ -180,22 +194,29 @@ __global__ __launch_bounds__(kThreads) void resize_kernel(const PagesArgs a) {
   }
 }
 
-// The same in three launches.
-__global__ __launch_bounds__(kThreads) void resize_sums_kernel(const PagesArgs a) {
-  int64_t top;
-  settle(a, offsets_in(a.offsets, a.batch), top);
-  if (threadIdx.x == 0) a.offsets[3 * (a.batch + 1)] = (int)top;
+// Two launches (batch up to kThreads): pages, then rows.  The first changes nothing that
+// its sums come from: lengths and counts are the second's.
+__global__ __launch_bounds__(kThreads) void resize_pages_kernel(const PagesArgs a) {
+  __shared__ int32_t sums[3 * (kThreads + 1)];
+  const Offsets o = offsets_in(sums, a.batch);
+  const Verdict v = settle<false>(a, o);
+  __syncthreads();
+  const int nback = (int)v.total.back, ntake = (int)v.total.taken;
+  for (int f = blockIdx.x * kThreads + threadIdx.x; f < (nback > ntake ? nback : ntake); f += gridDim.x * kThreads)
+    move_page(a, o, nback, ntake, v.top, f);
+  if (blockIdx.x) return;
+  if (threadIdx.x <= a.batch) a.offsets[threadIdx.x] = o.rows[threadIdx.x];
+  if (threadIdx.x == 0) {
+    a.offsets[a.batch] = o.rows[a.batch];
+    a.offsets[a.batch + 1] = v.status;
+    a.offsets[a.batch + 2] = (int)(v.top - v.total.taken);
+  }
 }
-__global__ __launch_bounds__(256) void resize_move_kernel(const PagesArgs a) {
-  const Offsets o = offsets_in(a.offsets, a.batch);
-  const int nback = o.back[a.batch], ntake = o.taken[a.batch], top = a.offsets[3 * (a.batch + 1)];
-  for (int f = blockIdx.x * 256 + threadIdx.x; f < (nback > ntake ? nback : ntake); f += gridDim.x * 256)
-    move_page(a, o, nback, ntake, top, f);
-}
-__global__ __launch_bounds__(256) void resize_map_kernel(const PagesArgs a) {
-  const Offsets o = offsets_in(a.offsets, a.batch);
-  const int new_rows = o.rows[a.batch], r0 = (blockIdx.x * 256 + threadIdx.x) * 4;
+
+// Position and slot of four rows from r0 on.
+__device__ inline void map_rows(const PagesArgs& a, const Offsets& o, int r0) {
   if (r0 >= a.rows) return;
+  const int new_rows = o.rows[a.batch];
   int b = r0 < new_rows ? owner(o.rows, a.batch, r0) : -1;
   int pos[4];
   int64_t slot[4];
@@ -215,11 +236,42 @@ __global__ __launch_bounds__(256) void resize_map_kernel(const PagesArgs a) {
     }
 }
 
+__global__ __launch_bounds__(256) void resize_rows_kernel(const PagesArgs a) {
+  __shared__ int32_t rows[kThreads + 1];
+  const int B = a.batch, status = a.offsets[B + 1];
+  for (int i = threadIdx.x; i <= B; i += 256) {
+    rows[i] = a.offsets[i];
+    if (blockIdx.x == 0) {
+      if (a.cu_q) a.cu_q[i] = rows[i];
+      if (i < B && status == 0) a.lens[i] = a.want[i];
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) set_counts(a, status, a.offsets[B + 2]);
+  __syncthreads();
+  map_rows(a, {nullptr, nullptr, rows}, (blockIdx.x * 256 + threadIdx.x) * 4);
+}
+
+// Three launches, for any batch.
+__global__ __launch_bounds__(kThreads) void resize_sums_kernel(const PagesArgs a) {
+  const Verdict v = settle<true>(a, offsets_in(a.offsets, a.batch));
+  if (threadIdx.x == 0) a.offsets[3 * (a.batch + 1)] = (int)v.top;
+}
+__global__ __launch_bounds__(256) void resize_move_kernel(const PagesArgs a) {
+  const Offsets o = offsets_in(a.offsets, a.batch);
+  const int nback = o.back[a.batch], ntake = o.taken[a.batch], top = a.offsets[3 * (a.batch + 1)];
+  for (int f = blockIdx.x * 256 + threadIdx.x; f < (nback > ntake ? nback : ntake); f += gridDim.x * 256)
+    move_page(a, o, nback, ntake, top, f);
+}
+__global__ __launch_bounds__(256) void resize_map_kernel(const PagesArgs a) {
+  map_rows(a, offsets_in(a.offsets, a.batch), (blockIdx.x * 256 + threadIdx.x) * 4);
+}
+
 // One workgroup up to this many sequences and new rows.  Two changes of 64 sequences, us in
-// one : three launches: 33 rows 12.3 : 16.2, 2850 14.1 : 16.9, 4795 15.4 : 17.7, 11003 19.9
-// : 18.3 (300 sequences and 375000 rows each: 1630 : 33).  It moves 1024 pages at a time,
-// so a call of few rows that ends many long sequences at once takes longer in it.
-constexpr int kOneBatch = kThreads, kOneRows = 8192;
+// one : two launches: 357 rows 12.3 : 14.6, 2850 14.0 : 15.1, 4795 15.4
+// : 15.4, 11003 19.9 : 15.5; of 300 sequences and 375000 rows each 1630 : 26 (33 in three).
+// It moves 1024 pages at a time, so a call of few rows that ends many long sequences at
+// once takes longer in it.
+constexpr int kOneBatch = kThreads, kOneRows = 4096;
 
 }  // namespace
 
@@ -232,12 +284,18 @@ wq_status launch_resize(const PagesArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(resize_kernel, dim3(1), dim3(kThreads), 0, s, a);
     return launch_status();
   }
-  hipLaunchKernelGGL(resize_sums_kernel, dim3(1), dim3(kThreads), 0, s, a);
   const int64_t most = (int64_t)a.batch * a.max_pages < a.num_pages ? (int64_t)a.batch * a.max_pages : a.num_pages;
+  const int map = (a.rows + 1023) / 1024;
+  if (a.batch <= kOneBatch) {
+    const int64_t wgs = (most + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(resize_pages_kernel, dim3((int)(wgs < 1 ? 1 : wgs < 64 ? wgs : 64)), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL(resize_rows_kernel, dim3(a.positions || a.slots ? map : 1), dim3(256), 0, s, a);
+    return launch_status();
+  }
+  hipLaunchKernelGGL(resize_sums_kernel, dim3(1), dim3(kThreads), 0, s, a);
   const int64_t wgs = (most + 255) / 256;
   if (wgs) hipLaunchKernelGGL(resize_move_kernel, dim3((int)(wgs < 1024 ? wgs : 1024)), dim3(256), 0, s, a);
-  if (a.rows && (a.positions || a.slots))
-    hipLaunchKernelGGL(resize_map_kernel, dim3((a.rows + 1023) / 1024), dim3(256), 0, s, a);
+  if (a.rows && (a.positions || a.slots)) hipLaunchKernelGGL(resize_map_kernel, dim3(map), dim3(256), 0, s, a);
   return launch_status();
 }
 
