@@ -203,7 +203,10 @@ LORA = [([1], 128, [16], 8, 1, False), ([1], 4096, [4096], 16, 8, False), ([1] *
         ([500, 3], 2176, [80], 16, 2, False),
         # many rows: several blocks of columns to a workgroup, several parts of K
         ([700, 600], 128, [16384], 64, 2, False), ([651, 1, 649], 1152, [8192, 8192], 16, 3, True),
-        ([1290], 128, [15984, 400], 128, 1, False)]
+        ([1290], 128, [15984, 400], 128, 1, False),
+        # many short sequences: many adapters to a tile of rows
+        ([1] * 300, 1152, [208, 32], 16, 40, True), ([2] * 170, 640, [96], 24, 100, False), ([1] * 1100, 256, [80, 48], 16, 90, True),
+        ([3] * 400, 1152, [64], 64, 7, True), ([1] * 700 + [900], 256, [144], 32, 2, False)]
 
 
 @pytest.mark.parametrize("case", LORA, ids=[f"{sum(c[0])}x{c[1]}-r{c[3]}" for c in LORA])

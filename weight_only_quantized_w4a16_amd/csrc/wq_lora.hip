@@ -28,19 +28,32 @@ namespace {
 // Shape of a call, a function of the sizes the host knows.
 struct LoraPlan {
   int few;     // the first product row by row
-  int groups;  // workgroups that share a tile's work items
+  int groups;  // workgroups that share a tile's work items, second product
+  int first;   // and first product
   int splits;  // parts of K
   int blocks;  // blocks of 128 columns per workgroup (second product)
 };
-LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0) {
+// (Where `part` lies and how long it is follows from the first four alone.)
+LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0, int kinds = 1) {
   LoraPlan p;
-  // Up to 256 rows row by row (us against tiles of 64 rows: 128 rows of 200 adapters of
-  // rank 64 60 : 72, of one adapter 17 : 24; 300 rows of 4 adapters of rank 8 21.5 :
-  // 19.4, of rank 64 43 : 23).
-  p.few = rows <= 256;
-  p.groups = !p.few ? 1 : batch < 64 ? batch : 64;
+  // Up to 256 rows row by row, and up to 1024 of sequences of one or two (us against tiles
+  // of 64 rows: 128 rows of 200 adapters of rank 64 56 : 72, of one adapter 17 : 15; 256
+  // rows 82 : 110 and 26 : 17; 300 rows of 4 sequences of rank 64 43 : 20; single rows of
+  // 100 adapters of rank 16 37 : 55 (300 rows), 101 : 160 (1000), 360 : 544 (4000), of 8
+  // adapters of rank 64 38 : 36, 88 : 67, 383 : 189).
+  p.few = rows <= 256 || (rows <= 1024 && (int64_t)batch * 2 >= rows);
+  if (p.few) {
+    p.first = p.groups = batch < 64 ? batch : 64;
+  } else {
+    // as many workgroups as a tile has sequences on average, or as there are adapters (and
+    // none); the first product one more, which most tiles of prompts send home, so that a
+    // tile of two takes no longer than the others
+    const int64_t seqs = (int64_t)batch * 64 / rows, most = kinds < 64 ? kinds : 64;
+    p.groups = (int)(seqs < 1 ? 1 : seqs > most ? most : seqs);
+    p.first = p.groups + (batch > 1 && p.groups < most);
+  }
   const int64_t tiles = ((int64_t)rows + 63) / 64, width = p.few ? 16 : 64;
-  const int64_t wgs = tiles * p.groups * ((columns + width - 1) / width);
+  const int64_t wgs = tiles * (p.few ? p.groups : 1) * ((columns + width - 1) / width);
   if (p.few) {
     // about 1024 workgroups, of which those without an item leave at once, and 1024 of K
     // to each (64 tokens of 40 adapters: 10.9 us, 12.9 with 2048, 19.3 with 4096)
@@ -850,10 +863,10 @@ wq_status launch(const LoraArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((lora_fused_kernel<DT>), grid, block, 0, s, a, blocks);
     return launch_status();
   }
-  const LoraPlan p = lora_plan(a.seqs.rows, a.seqs.batch, a.K, columns, a.N);
+  const LoraPlan p = lora_plan(a.seqs.rows, a.seqs.batch, a.K, columns, a.N, a.num + (a.y != a.out));
   const int tiles = (a.seqs.rows + 63) / 64, kc = (a.rank + 31) / 32;
   const int width = p.few ? 16 : 64;
-  const dim3 grid(tiles, (columns + width - 1) / width * p.splits, p.groups), block(256);
+  const dim3 grid(tiles, (columns + width - 1) / width * p.splits, p.first), block(256);
   if (p.few) hipLaunchKernelGGL((lora_shrink_rows_kernel<DT>), grid, block, 0, s, a, p.splits);
   else hipLaunchKernelGGL((lora_shrink_kernel<DT>), grid, block, 0, s, a, p.splits);
   if (!p.few) hipLaunchKernelGGL((lora_split_kernel<DT>), dim3((a.seqs.rows + 15) / 16, a.slices), block, 0, s, a, p.splits);
