@@ -206,7 +206,10 @@ LORA = [([1], 128, [16], 8, 1, False), ([1], 4096, [4096], 16, 8, False), ([1] *
         ([1290], 128, [15984, 400], 128, 1, False),
         # many short sequences: many adapters to a tile of rows
         ([1] * 300, 1152, [208, 32], 16, 40, True), ([2] * 170, 640, [96], 24, 100, False), ([1] * 1100, 256, [80, 48], 16, 90, True),
-        ([3] * 400, 1152, [64], 64, 7, True), ([1] * 700 + [900], 256, [144], 32, 2, False)]
+        ([3] * 400, 1152, [64], 64, 7, True), ([1] * 700 + [900], 256, [144], 32, 2, False),
+        # few rows of one or two sequences: several items of an adapter
+        ([16], 640, [272], 16, 3, False), ([9, 4], 384, [96, 32], 24, 2, True), ([64], 1152, [528], 32, 2, False),
+        ([90, 38], 256, [64], 128, 3, True), ([250], 1024, [144, 48], 16, 2, False), ([5] * 50, 384, [96], 40, 30, True)]
 
 
 @pytest.mark.parametrize("case", LORA, ids=[f"{sum(c[0])}x{c[1]}-r{c[3]}" for c in LORA])

@@ -33,17 +33,27 @@ struct LoraPlan {
   int splits;  // parts of K
   int blocks;  // blocks of 128 columns per workgroup (second product)
 };
+// Items of up to four rows that a tile of 64 rows has, with sequences of one length and an
+// adapter to each: what a workgroup of their own is launched for (more are taken in turn;
+// with as many workgroups as sequences 64 rows of one sequence took 47 us, now 9.5).
+int few_items(int rows, int batch) {
+  const int tile = rows < 64 ? rows : 64;
+  const int64_t seqs = ((int64_t)batch * tile + rows - 1) / rows;
+  return seqs < tile ? (int)seqs + (tile - (int)seqs) / 4 : tile;
+}
 // (Where `part` lies and how long it is follows from the first four alone.)
 LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0, int kinds = 1) {
   LoraPlan p;
-  // Up to 256 rows row by row, and up to 1024 of sequences of one or two (us against tiles
-  // of 64 rows: 128 rows of 200 adapters of rank 64 56 : 72, of one adapter 17 : 15; 256
-  // rows 82 : 110 and 26 : 17; 300 rows of 4 sequences of rank 64 43 : 20; single rows of
-  // 100 adapters of rank 16 37 : 55 (300 rows), 101 : 160 (1000), 360 : 544 (4000), of 8
-  // adapters of rank 64 38 : 36, 88 : 67, 383 : 189).
-  p.few = rows <= 256 || (rows <= 1024 && (int64_t)batch * 2 >= rows);
+  // Row by row up to 128 rows, and up to 1024 where there are not many to a sequence, else
+  // in tiles of 64 (us, ranks 16 and 64; 4096 -> 6144): 128 single rows of 200 adapters 27 56
+  // : 37 72, of one adapter 11 17 : 13 15; 256 rows of 200 adapters 41 82 : 57 110, of
+  // sequences of 16 rows 14 20 : 16 20, of one sequence 13 19 : 14 17; 300 rows, five to a
+  // sequence 20 40 : 26 39; 1000 single rows of 100 adapters 101 258 : 161 344, of 8 adapters
+  // 39 88 : 40 67, five to a sequence 48 125 : 51 100; 4000 rows 360 974 : 544 1071 and 151 383
+  // : 106 189.
+  p.few = rows <= 128 || (rows <= 1024 && (int64_t)rows * rows <= (int64_t)3000 * batch);
   if (p.few) {
-    p.first = p.groups = batch < 64 ? batch : 64;
+    p.first = p.groups = few_items(rows, batch);
   } else {
     // as many workgroups as a tile has sequences on average, or as there are adapters (and
     // none); the first product one more, which most tiles of prompts send home, so that a
@@ -854,7 +864,7 @@ template <int DT>
 wq_status launch(const LoraArgs& a, hipStream_t s) {
   const int columns = a.slices * a.rank;
   if (lora_fused(a.seqs.rows, a.K, a.rank)) {
-    const int groups = a.seqs.batch < 64 ? a.seqs.batch : 64;
+    const int groups = few_items(a.seqs.rows, a.seqs.batch);
     int blocks = (a.N + 255) / 256 * groups / 128;  // (128 workgroups: 16 rows of 16 adapters 11.8 us, 256 18.7)
     blocks = blocks < 1 ? 1 : blocks > 16 ? 16 : blocks;
     int chunks = 0;
