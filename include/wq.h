@@ -387,8 +387,9 @@ wq_status wq_kv_attention(const void* q, int64_t ld_q, wq_dtype dt, const void* 
  *   eps      : a positive normal fp32 number
  * y or sum may be x or residual themselves (with their stride); other shared
  * elements are WQ_EINVAL.  dim % 8 == 0, 8 <= dim <= 65536, heads <= 4096,
- * rows <= 2^24, rows heads <= 2^28, rows heads dim <= 2^33 (else WQ_EUNSUPPORTED).  The sum of squares must
- * stay within fp32: past it finite elements give 0, as in that arithmetic.
+ * rows <= 2^24, rows heads <= 2^28, rows heads dim <= 2^33 (else WQ_EUNSUPPORTED).
+ * The sum of squares must stay within fp32: past it finite elements give 0, as in
+ * that arithmetic.
  */
 wq_status wq_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight,
                       float eps, wq_dtype dt, void* y, int64_t ld_y, void* sum, int64_t ld_sum, int rows, int heads,
@@ -441,8 +442,8 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
  *   ws       : wq_lora_workspace_bytes() bytes for these sizes, 16-byte aligned (may be
  *              NULL when 0); calls that overlap in time must not share it
  * All pointers but adapters, scales, ranks and cu_q are 16-byte aligned.  K % 128 == 0,
- * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24, rows N <= 2^38 (else
- * WQ_EUNSUPPORTED).
+ * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24,
+ * rows N <= 2^38 (else WQ_EUNSUPPORTED).
  * Rows outside every sequence are left as they were.  fp32 accumulation; x A^T enters
  * the second product in two parts that hold it to 2^-16 (bf16) or 2^-22 (fp16) of the
  * row's largest; out is rounded to `dt` once.  The same call gives the same bits.
