@@ -439,8 +439,9 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
  *              16, the last one N; slices <= 4
  *   adapters : device int32 [batch]; a sequence whose number is not in 0 ..
  *              num_adapters - 1 has none: its rows are y
- *   ws       : wq_lora_workspace_bytes() bytes for these sizes, 16-byte aligned (may be
- *              NULL when 0); calls that overlap in time must not share it
+ *   ws       : wq_lora_workspace_bytes() bytes for these sizes (fewer rows may need
+ *              more), 16-byte aligned (may be NULL when 0); calls that overlap in time
+ *              must not share it; nothing in it needs to start at any value
  * All pointers but adapters, scales, ranks and cu_q are 16-byte aligned.  K % 128 == 0,
  * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24,
  * rows N <= 2^38 (else WQ_EUNSUPPORTED).
