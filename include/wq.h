@@ -480,7 +480,8 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
  *   slots     : int64 [rows], its page * page_size + position % page_size
  *               Rows past the new ones are -1; new rows past `rows` are not written.
  *   ws        : wq_kv_resize_workspace_bytes() bytes, 16-byte aligned (NULL when 0)
- * page_size as for the cache; batch <= 2^16, rows <= 2^24, max_pages page_size <= 2^30.
+ * page_size as for the cache; batch <= 2^16, rows <= 2^24, max_pages page_size <= 2^30,
+ * num_pages <= 2^30 (else WQ_EUNSUPPORTED).
  */
 size_t wq_kv_resize_workspace_bytes(int batch, int max_pages, int num_pages, int rows);
 wq_status wq_kv_resize(int32_t* block_table, int32_t* kv_lens, const int32_t* want_lens, int32_t* free_pages,

@@ -66,6 +66,9 @@ struct PagesArgs {
   int32_t* offsets;    // workspace: back [batch + 1], taken [batch + 1], new rows [batch + 1]
   int rows, batch, max_pages, num_pages, page_shift;
 };
+// Pages of a table: a thread's next one is up to 2^18 further, in 32 bits (and a cache of
+// 2^30 pages, 1152 bytes each at least, would be 1.2 TB).
+constexpr int kMaxPages = 1 << 30;
 size_t pages_workspace_bytes(int batch, int max_pages, int num_pages, int rows);
 wq_status launch_resize(const PagesArgs& a, hipStream_t s);
 

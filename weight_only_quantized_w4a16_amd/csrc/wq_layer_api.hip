@@ -213,7 +213,9 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
 }
 
 size_t wq_kv_resize_workspace_bytes(int batch, int max_pages, int num_pages, int rows) {
-  if (batch < 0 || batch > (1 << 16) || max_pages < 0 || num_pages <= 0 || rows < 0 || rows > (1 << 24)) return 0;
+  if (batch < 0 || batch > (1 << 16) || max_pages < 0 || num_pages <= 0 || num_pages > kMaxPages || rows < 0 ||
+      rows > (1 << 24))
+    return 0;
   return pages_workspace_bytes(batch, max_pages, num_pages, rows);
 }
 
@@ -222,7 +224,8 @@ wq_status wq_kv_resize(int32_t* block_table, int32_t* kv_lens, const int32_t* wa
                        int max_pages, int num_pages, int page_size, void* ws, size_t ws_bytes, void* stream) {
   if (rows < 0 || batch < 0 || max_pages < 0 || num_pages <= 0 || page_size <= 0) return WQ_EINVAL;
   if (!power_of_two(page_size) || page_size < 16 || page_size > 1024) return WQ_EUNSUPPORTED;
-  if (rows > (1 << 24) || batch > (1 << 16) || (int64_t)max_pages * page_size > ((int64_t)1 << 30))
+  if (rows > (1 << 24) || batch > (1 << 16) || (int64_t)max_pages * page_size > ((int64_t)1 << 30) ||
+      num_pages > kMaxPages)
     return WQ_EUNSUPPORTED;
   if (!free_pages || !counts || (batch > 0 && (!kv_lens || !want_lens || (max_pages > 0 && !block_table))))
     return WQ_EINVAL;

@@ -31,7 +31,8 @@ class KVPages:
         _need(isinstance(self.block_table, torch.Tensor) and self.block_table.dim() == 2,
               "block_table must be a [batch][pages] tensor")
         dev, (batch, _) = self.block_table.device, self.block_table.shape
-        _need(isinstance(self.num_pages, int) and 0 < self.num_pages < 1 << 31, "num_pages must be a positive count")
+        _need(isinstance(self.num_pages, int) and 0 < self.num_pages <= 1 << 30,
+              "num_pages must be a positive count up to 2^30")
         _need(isinstance(self.page_size, int) and 16 <= self.page_size <= 1024
               and self.page_size & (self.page_size - 1) == 0, "page_size must be a power of two from 16 to 1024")
         _check_tensor(self.block_table, "block_table", (torch.int32,), self.block_table.shape)
@@ -42,7 +43,7 @@ class KVPages:
 
 def wq_kv_pages(num_pages: int, page_size: int, batch: int, max_pages: int, device="cuda") -> KVPages:
     """`num_pages` free pages and `batch` empty sequences of at most `max_pages` pages each."""
-    _need(isinstance(num_pages, int) and 0 < num_pages < 1 << 31, "num_pages must be a positive count")
+    _need(isinstance(num_pages, int) and 0 < num_pages <= 1 << 30, "num_pages must be a positive count up to 2^30")
     i32 = dict(dtype=torch.int32, device=device)
     return KVPages(torch.full((batch, max_pages), -1, **i32), torch.zeros(batch, **i32),
                    torch.arange(num_pages - 1, -1, -1, **i32), torch.tensor([num_pages, 0], **i32), num_pages, page_size)
