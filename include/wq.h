@@ -442,7 +442,8 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
  *   ws       : wq_lora_workspace_bytes() bytes for these sizes (fewer rows may need
  *              more), 16-byte aligned (may be NULL when 0); calls that overlap in time
  *              must not share it; nothing in it needs to start at any value
- * All pointers but adapters, scales, ranks and cu_q are 16-byte aligned.  K % 128 == 0,
+ * Neither out nor ws shares memory with scales, ranks, adapters or cu_q (WQ_EINVAL),
+ * which are 4-byte aligned, all other pointers 16-byte.  K % 128 == 0,
  * N % 16 == 0, K and N up to 2^20, rank a multiple of 8 up to 128, rows <= 2^24,
  * rows N <= 2^38 (else WQ_EUNSUPPORTED).
  * Rows outside every sequence are left as they were.  fp32 accumulation; x A^T enters

@@ -195,6 +195,16 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
   if (bytes_meet(ws, need, out, ny) || bytes_meet(ws, need, x, (size_t)rows * K * 2) || bytes_meet(ws, need, y, ny) ||
       bytes_meet(ws, need, a, na) || bytes_meet(ws, need, b, nb))
     return WQ_EINVAL;
+  // (every workgroup reads these, and the second product again)
+  const size_t each = (size_t)num_adapters * 4, per = (size_t)batch * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } small[] = {{scales, each}, {ranks, each}, {adapters, per}, {cu_q, per + 4}};
+  for (const auto& m : small) {
+    if ((uintptr_t)m.p & 3) return WQ_EUNSUPPORTED;
+    if (bytes_meet(m.p, m.n, out, ny) || bytes_meet(m.p, m.n, ws, need)) return WQ_EINVAL;
+  }
   r.x = (const uint16_t*)x;
   r.a = (const uint16_t*)a;
   r.b = (const uint16_t*)b;
