@@ -414,6 +414,8 @@ wq_status wq_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t
  *              row for all axes), for every row; kv_lens and cu_q are not read then.
  *              NULL: positions of sequences, the same on every axis, and rows outside
  *              every sequence are left as they were
+ * No output shares memory with turns (8-byte aligned), axis, positions, kv_lens or cu_q
+ * (4-byte) where they are read (WQ_EINVAL).
  * head_dim % 8 == 0 and <= 512; rotary_dim <= head_dim, a multiple of 16 (of 8 with
  * adjacent pairs); axes <= 16; heads <= 4096 (else WQ_EUNSUPPORTED).  Angles are
  * exact to 2^-28 of a turn; fp32 arithmetic, outputs rounded to `dt` once.

@@ -1,7 +1,7 @@
 """Limits of the layer operators' entry points, and overlaps with the small arrays they read (CPU: nothing is launched)."""
 import pytest
 
-from test_layer_checks import L, lora_call, resize_call  # noqa: F401  (L is a fixture)
+from test_layer_checks import L, lora_call, norm_call, resize_call, rotary_call  # noqa: F401  (L is a fixture)
 import weight_only_quantized_w4a16_amd as wq
 
 
@@ -38,3 +38,39 @@ def test_lora_refuses_outputs_over_what_it_still_reads(L):
         assert lora_call(L, **{**small, name: out + 4 - size[name]}, rows=100, out=out) == 1, name
         if name != "cu":
             assert lora_call(L, **{**small, name: out - size[name], "cu": at + 12290}, rows=100, out=out) == 2, name
+
+
+def test_rotary_refuses_outputs_over_what_it_still_reads(L):
+    """The plan, positions, lengths and offsets are read by every row's threads."""
+    rows, ld, at = 4, 1536, 4 << 20                           # rows of 8 (queries) and 2 heads of 128
+    size = dict(turns=64 * 8, axis=64 * 4, lens=2 * 4, cu=3 * 4, pos=rows * 4)
+    arrays = {name: (8 << 20) + 4096 * i for i, name in enumerate(size)}
+    for name in size:
+        args = dict(arrays, **({"lens": None, "cu": None} if name == "pos" else {"pos": None}))
+        for out, width in (("qo", 8 * 128 * 2), ("ko", 2 * 128 * 2)):
+            place = dict(qo=6 << 20, ko=7 << 20)
+            place[out] = at
+            for row in range(rows):
+                first, end = at + row * ld * 2, at + row * ld * 2 + width
+                for p in (first + 8 - size[name], first, end - 8):
+                    assert rotary_call(L, **{**args, name: p}, **place) == 1, (name, out, row, p - first)
+        for off in (1, 2, 3):
+            assert rotary_call(L, **{**args, name: arrays[name] + off}, qo=6 << 20, ko=7 << 20) == 2, (name, off)
+    # in front of an output, between its rows and behind it: it is then the positions' alignment that is refused
+    args = dict(arrays, lens=None, cu=None, pos=arrays["pos"] + 2, qo=at, ko=7 << 20)
+    for name in ("turns", "axis"):
+        for p in (at - size[name], at + 2048, at + ld * 2 - size[name], at + 3 * ld * 2 + 2048):
+            assert rotary_call(L, **{**args, name: p}) == 2, (name, p - at)
+    # positions of several axes, 1 MiB apart
+    args = dict(arrays, lens=None, cu=None, axes=3, ld_pos=1 << 18, qo=16 << 20, ko=17 << 20)
+    for out in (16 << 20, 17 << 20):
+        for ax in range(3):
+            assert rotary_call(L, **{**args, "pos": out - ax * (1 << 20) + 8}) == 1
+    # lengths are not read beside positions, and not looked at then
+    assert rotary_call(L, **dict(arrays, lens=4 << 20, cu=None, pos=arrays["pos"] + 2, qo=4 << 20, ko=7 << 20)) == 2
+
+
+def test_norm_refuses_outputs_over_its_weight(L):
+    for y, w, code in ((2 << 20, (2 << 20) + 7 * 2048 + 2048 - 16, 1), (2 << 20, (2 << 20) - 256 + 16, 1),
+                       (2 << 20, (2 << 20) - 256 + 8, 1), (2 << 20, (2 << 20) - 256 - 8, 2), (2 << 20, (2 << 20) + 8 * 2048 + 8, 2)):
+        assert norm_call(L, y=y, w=w, rows=8) == code, (y, w)

@@ -39,12 +39,13 @@ bool clash(const Rows& out, const Rows& in, int rows, bool in_place) {
   if (in_place && out.p == in.p && out.width == in.width && (rows == 1 || out.ld == in.ld)) return false;
   return rows_meet(out.p, out.ld, out.width, in.p, in.ld, in.width, rows);
 }
-// Whether a row matrix meets a plain range (both 16-byte aligned).
-bool range_meets(const Rows& m, int rows, const void* p, int n) {
-  if (!m.p) return false;
+// Whether a row matrix meets a plain range of n bytes.
+bool range_meets(const Rows& m, int rows, const void* p, int64_t n) {
+  if (!m.p || !p || n <= 0) return false;
   typedef __int128 Z;
-  const Z d = ((Z)(uintptr_t)p - (Z)(uintptr_t)m.p) / 2, ld = rows > 1 ? m.ld : m.width;
-  const Z i = d < m.width ? 0 : (d - m.width) / ld + 1;  // the first row that ends behind the range's beginning
+  const Z d = (Z)(uintptr_t)p - (Z)(uintptr_t)m.p, w = (Z)m.width * 2, ld = rows > 1 ? (Z)m.ld * 2 : w;
+  if (d + n <= 0 || d >= (rows - 1) * ld + w) return false;
+  const Z i = d < w ? 0 : (d - w) / ld + 1;  // the first row that ends behind the range's beginning
   return i < rows && i * ld < d + n;
 }
 
@@ -72,7 +73,7 @@ wq_status wq_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t
   const Rows X{x, ld_x, width}, R{residual, ld_residual, width}, Y{y, ld_y, width}, S{sum, ld_sum, width};
   for (const Rows& out : {Y, S}) {
     if (clash(out, X, rows, true) || clash(out, R, rows, true)) return WQ_EINVAL;
-    if (range_meets(out, rows, weight, dim)) return WQ_EINVAL;
+    if (range_meets(out, rows, weight, (int64_t)dim * 2)) return WQ_EINVAL;
   }
   if (clash(Y, S, rows, false)) return WQ_EINVAL;
   if ((uintptr_t)weight & 15) return WQ_EUNSUPPORTED;
@@ -131,6 +132,22 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
       clash(KO, Q, rows, false) || clash(QO, KO, rows, false))
     return WQ_EINVAL;
   if ((uintptr_t)turns & 7) return WQ_EUNSUPPORTED;
+  // (every row's threads read these)
+  const int64_t pairs = rotary_dim / 2, per = (int64_t)batch * 4, step = axes > 1 ? ld_positions : 0;
+  const struct {
+    const void* p;
+    int64_t n;
+  } small[] = {{turns, pairs * 8}, {axis, pairs * 4}, {positions ? nullptr : kv_lens, per},
+               {positions ? nullptr : cu_q, per + 4}};
+  for (const auto& m : small) {
+    if ((uintptr_t)m.p & 3) return WQ_EUNSUPPORTED;
+    if (range_meets(QO, rows, m.p, m.n) || range_meets(KO, rows, m.p, m.n)) return WQ_EINVAL;
+  }
+  if ((uintptr_t)positions & 3) return WQ_EUNSUPPORTED;
+  for (int ax = 0; positions && ax < (step ? axes : 1); ++ax) {
+    const int32_t* p = positions + ax * step;
+    if (range_meets(QO, rows, p, (int64_t)rows * 4) || range_meets(KO, rows, p, (int64_t)rows * 4)) return WQ_EINVAL;
+  }
   a.x[0] = (const uint16_t*)q;
   a.x[1] = (const uint16_t*)k;
   a.y[0] = (uint16_t*)q_out;
