@@ -473,9 +473,10 @@ wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, cons
  *   free_pages : device int32 [num_pages]; counts: device int32 [2], the first the number
  *                of free pages
  * All or nothing: where the free pages do not suffice, or a wanted length is below 0 or
- * past the table, or more pages come back than there are, nothing is changed; counts[1]
- * is 0, the number of pages lacking, or -1.  kv_lens, want_lens, block_table, free_pages
- * and counts share no memory with each other or with an output (WQ_EINVAL).
+ * past the table, or more pages come back than there are, or all sequences together get
+ * more than 2^31 - 1 new tokens, nothing is changed; counts[1] is 0, the number of pages
+ * lacking, or -1 for the others.  kv_lens, want_lens, block_table, free_pages and counts
+ * share no memory with each other or with an output (WQ_EINVAL).
  * Outputs (each may be NULL), for the step that fills the new tokens:
  *   cu_q      : int32 [batch + 1], offsets of the new rows (as every call takes them);
  *               all 0 where nothing was changed

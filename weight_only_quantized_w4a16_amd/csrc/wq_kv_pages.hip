@@ -119,7 +119,8 @@ __device__ inline Verdict settle(const PagesArgs& a, const Offsets& o) {
   sum_before(own, at, total);
   bad = __syncthreads_or(bad);
   Verdict v = {total, count + total.back, 0};
-  if (bad || v.top > a.num_pages || total.rows > (1 << 24)) v.status = -1;
+  // (the offsets are 32-bit; within them the pages taken are no more than the rows)
+  if (bad || v.top > a.num_pages || total.rows > 0x7FFFFFFF) v.status = -1;
   else if (total.taken > v.top) v.status = (int)(total.taken - v.top);
   if (v.status) {
     v.total = at = {0, 0, 0};

@@ -58,8 +58,9 @@ def wq_kv_resize(pages: KVPages, want_lens: torch.Tensor, rows: int = 0, cu_q: O
                  positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, ws=None,
                  stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """The sequences of `pages` become want_lens (int32 [batch]) tokens long: pages are taken or given back, kv_lens,
-    the table, the free pages and counts are changed in place -- or, where the free pages do not suffice or a length has
-    no place in the table, nothing is but counts[1] (the pages lacking, or -1; 0 where all went well).
+    the table, the free pages and counts are changed in place -- or, where the free pages do not suffice, a length has no
+    place in the table or the new tokens are more than 2^31 - 1 in all, nothing is but counts[1] (the pages lacking, or
+    -1; 0 where all went well).
 
     Returns (cu_q, positions, slots): int32 [batch + 1] offsets of the new rows (all 0 where nothing was changed),
     int32 [rows] position and int64 [rows] slot (page * page_size + place in it) of each; `rows` is how many the
