@@ -450,7 +450,8 @@ wq_status wq_rotary(const void* q, int64_t ld_q, const void* k, int64_t ld_k, wq
  * rows N <= 2^38 (else WQ_EUNSUPPORTED).
  * Rows outside every sequence are left as they were.  fp32 accumulation; x A^T enters
  * the second product in two parts that hold it to 2^-16 (bf16) or 2^-22 (fp16) of the
- * row's largest; out is rounded to `dt` once.  The same call gives the same bits.
+ * row's largest finite one (an infinite entry of b so gives NaN, infinity times a part
+ * that may be 0); out is rounded to `dt` once.  The same call gives the same bits.
  */
 size_t wq_lora_workspace_bytes(int rows, int batch, int K, int rank, int slices);
 wq_status wq_lora(const void* x, wq_dtype dt, const void* a, const void* b, const float* scales, const int32_t* ranks,

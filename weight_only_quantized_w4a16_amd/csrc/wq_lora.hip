@@ -431,17 +431,22 @@ __device__ inline void two_parts(f4 v0, f4 v1, float up, u32x4& hi, u32x4& lo) {
     lo[q] = pack2<DT>(__builtin_isinf(h0) ? 0.f : x0 - h0, __builtin_isinf(h1) ? 0.f : x1 - h1);
   }
 }
+// The largest finite one: beside an infinity the others must stay within fp16 too, or
+// they would be infinities of either sign.
 __device__ inline float largest(f4 a, f4 b) {
   float m = 0.f;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) m = fmaxf(m, fmaxf(fabsf(a[q]), fabsf(b[q])));
+  for (int q = 0; q < 4; ++q) {
+    const float x = fabsf(a[q]), y = fabsf(b[q]);
+    m = fmaxf(m, fmaxf(x < __builtin_inff() ? x : 0.f, y < __builtin_inff() ? y : 0.f));
+  }
   return m;
 }
 // fp16: the power of two that takes a row's largest to 2^13 .. 2^14, and the one back,
-// both normal numbers
+// both normal numbers (m is below 2^53: 2^20 products of numbers below 2^16)
 __device__ inline void powers(float m, float& up, float& down) {
   int e = (int)(__float_as_uint(m) >> 23) - 127;
-  e = e < -100 ? -100 : e > 120 ? 13 : e;  // (tiny; an infinity or NaN is left as it is)
+  e = e < -100 ? -100 : e;  // (tiny)
   up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
   down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 }
