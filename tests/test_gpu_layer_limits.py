@@ -91,3 +91,89 @@ def test_an_infinite_weight_of_an_adapter(rows, rank, dtype):
     if cut < rows:
         want, bound = _layer.lora(x[cut:], y[cut:], a, b, scales, [rank, rank], (N,), [1] * (rows - cut))
         within(got[cut:], want, bound)
+
+
+# ---------------------------------------------------------------------------- numbers that are none
+def guarded(shape, dtype, fill):
+    """A tensor of `shape` in the middle of a larger buffer, all of it `fill`; and a check that the rest still is."""
+    n, guard = math.prod(shape), 1 << 16
+    whole = torch.full((n + 2 * guard,), fill, dtype=dtype, device="cuda")
+    return whole[guard:guard + n].view(shape), lambda: bool((whole[:guard] == fill).all() and (whole[guard + n:] == fill).all())
+
+
+ODD = [lambda n, T: [0] * (n + 1), lambda n, T: [1 << 30] * (n + 1), lambda n, T: [-2147483648] * (n + 1),
+       lambda n, T: [(-5, 3, 2, 9, 4, 1 << 30, 3)[i % 7] for i in range(n + 1)],
+       lambda n, T: [T - 7 * i for i in range(n + 1)], lambda n, T: [2147483647] * n + [-1]]
+
+
+@pytest.mark.parametrize("rows,batch,rank", [(12, 6, 16), (70, 6, 16), (70, 90, 24), (1300, 6, 16), (1300, 90, 64), (700, 700, 8)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_offsets_that_are_none_stay_within_the_buffers(rows, batch, rank, dtype):
+    """Nothing but the outputs and the scratch is written, whatever the offsets say; where they give no sequence a row,
+    no row is."""
+    g = torch.Generator().manual_seed(rows + batch)
+    K, N = 256, 80
+    x, y = randn(g, rows, K).to(dtype).cuda(), randn(g, rows, N).to(dtype).cuda()
+    bank = wq.LoraBank(randn(g, 4, 1, rank, K).to(dtype).cuda(), randn(g, 4, N, rank).to(dtype).cuda(),
+                       torch.ones(4, device="cuda"))
+    ids, lens = i32([b % 6 - 1 for b in range(batch)]), i32([b % 9 for b in range(batch)])
+    plan, q, k = wq.wq_rotary_plan(64), randn(g, rows, 3, 64).to(dtype).cuda(), randn(g, rows, 1, 64).to(dtype).cuda()
+    need = wq.wq_lora_workspace_bytes(rows, batch, K, rank)
+    for i, odd in enumerate(ODD):
+        cu = i32(odd(batch, rows))
+        out, out_kept = guarded((rows, N), dtype, 7.0)
+        ws, ws_kept = guarded((max(need, 16),), torch.uint8, 0xFF)
+        wq.wq_lora(x, bank, ids, y, cu_q=cu, out=out, ws=ws)
+        qo, q_kept = guarded((rows, 3, 64), dtype, 7.0)
+        ko, k_kept = guarded((rows, 1, 64), dtype, 7.0)
+        wq.wq_rotary(q, k, plan, kv_lens=lens, cu_q=cu, out=(qo, ko))
+        assert out_kept() and ws_kept() and q_kept() and k_kept(), i
+        if i < 3:
+            assert bool((out == 7).all()) and bool((qo == 7).all()) and bool((ko == 7).all()), i
+
+
+@pytest.mark.parametrize("rows,batch", [(40, 5), (6000, 5), (40, 1100)])
+def test_page_tables_that_are_none_stay_within_the_buffers(rows, batch):
+    """Lengths, counts and entries of the tables that make no sense: nothing but the tables and the outputs is written,
+    and the verdict is what the rules make of them."""
+    g = torch.Generator().manual_seed(rows + batch)
+    P, max_pages, num_pages = 16, 30, 400
+    pages_of = lambda n: -(-n // P)
+    some = torch.tensor([0, 1, 17, 400, 480, 481, -1, 1 << 30, 2147483647, -2147483648])
+    pick = lambda *shape: some[torch.randint(0, len(some), shape, generator=g)].to(torch.int32).cuda()
+    for step in range(20):
+        checks, t = [], {}
+        for name, shape, values in (("block_table", (batch, max_pages), pick(batch, max_pages)), ("kv_lens", (batch,), pick(batch)),
+                                    ("free", (num_pages,), pick(num_pages)), ("counts", (2,), pick(2))):
+            t[name], kept = guarded(shape, torch.int32, 7)
+            t[name].copy_(values)
+            checks.append(kept)
+        if step % 2:  # (not all of it at once: some of these are changes)
+            t["kv_lens"].copy_(torch.randint(0, 40, (batch,), generator=g))
+            t["counts"][0] = [0, 33, num_pages][step % 3]
+        if step % 4 == 3:
+            t["kv_lens"][5:] = 0
+        want = pick(batch)
+        if step % 4 > 1:
+            few = torch.rand(batch, generator=g) < 60 / batch
+            want = torch.where(few, torch.randint(0, 90, (batch,), generator=g), 0).to(torch.int32).cuda()
+        pages = wq.KVPages(**t, num_pages=num_pages, page_size=P)
+        outs = []
+        for n, dtype in ((batch + 1, torch.int32), (rows, torch.int32), (rows, torch.int64)):
+            o, kept = guarded((n,), dtype, 7)
+            outs.append(o)
+            checks.append(kept)
+        before = {name: v.clone() for name, v in t.items()}
+        wq.wq_kv_resize(pages, want, rows, *outs)
+        assert all(kept() for kept in checks), step
+        old, new = (before["kv_lens"].long().clamp(0, max_pages * P).tolist(), want.tolist())
+        moved = [pages_of(m) - pages_of(n) for n, m in zip(old, new)]
+        top = min(max(int(before["counts"][0]), 0), num_pages) - sum(d for d in moved if d < 0)
+        fails = any(not 0 <= m <= max_pages * P for m in new) or top > num_pages
+        status = -1 if fails else max(0, sum(d for d in moved if d > 0) - top)
+        assert int(t["counts"][1]) == status, step
+        if status:
+            assert all(torch.equal(t[n], before[n]) for n in ("block_table", "kv_lens", "free")) and not outs[0].any()
+        else:
+            assert torch.equal(t["kv_lens"], want) and outs[0].tolist() == [
+                sum(max(0, m - n) for n, m in zip(old[:b], new[:b])) for b in range(batch + 1)]
