@@ -50,14 +50,19 @@ LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0, int kinds
   // sequences of 16 rows 14 20 : 16 20, of one sequence 13 19 : 14 17; 300 rows, five to a
   // sequence 20 40 : 26 39; 1000 single rows of 100 adapters 101 258 : 161 344, of 8 adapters
   // 39 88 : 40 67, five to a sequence 48 125 : 51 100; 4000 rows 360 974 : 544 1071 and 151 383
-  // : 106 189.
+  // : 106 189.  Rank and number of adapters are not in the rule, and where they decide it
+  // is up to a third off: 1000 single rows of 8 adapters of rank 64 run in the 88 of these,
+  // 128 single rows of one adapter of that rank in the 17.
   p.few = rows <= 128 || (rows <= 1024 && (int64_t)rows * rows <= (int64_t)3000 * batch);
   if (p.few) {
     p.first = p.groups = few_items(rows, batch);
   } else {
     // as many workgroups as a tile has sequences on average, or as there are adapters (and
     // none); the first product one more, which most tiles of prompts send home, so that a
-    // tile of two takes no longer than the others
+    // tile of two takes no longer than the others.  The average suits neither part of a
+    // mixed batch: the tile of single tokens beside a prompt works through its adapters in
+    // turn (63 tokens of 40 adapters and 1000 rows of one more, ranks 16 and 64: 110 and
+    // 148 us; as two calls 19 + 19 and 31 + 24)
     const int64_t seqs = (int64_t)batch * 64 / rows, most = kinds < 64 ? kinds : 64;
     p.groups = (int)(seqs < 1 ? 1 : seqs > most ? most : seqs);
     p.first = p.groups + (batch > 1 && p.groups < most);
@@ -97,7 +102,13 @@ LoraPlan lora_plan(int rows, int batch, int K, int columns, int N = 0, int kinds
 // row of rank 16 7.3 : 6.3 (7.4 : 6.4), of rank 32 7.4 : 8.3, of 11008 -> 4096 8.6 : 8.5;
 // 16 rows of one adapter of rank 16 8.1 : 7.9, of many (11.5 : 11.6) to (14.4 : 11.8), of
 // rank 8 from 11008 9.4 : 11.3; 64 rows of one 10.1 : 11.6.  Not captured, the launch
-// and the workspace it saves are 3.5 us of host time.
+// and the workspace it saves are 3.5 us of host time, and that is why some shapes that
+// lose up to 1.9 us captured are in: rank 32 up to K = 2048 (one row 7.4 : 8.2, four of
+// four adapters 7.8 : 8.5, 16 of 16 8.6 : 10.3), four rows of one adapter from 8192 (8.7 :
+// 9.1) and 11008 (9.4 : 10.6), 16 rows of rank 8 from 8192 (8.8 : 10.6).  Up to rank 16 and
+// K = 2048 one launch gains everywhere (7.4 : 6.2 to 8.6 : 7.4).  Out of it: rank 32 from
+// 4096 (one row 7.6 : 8.3, 16 rows of 16 9.5 : 12.3) and 11008 (8.8 : 12.5), 16 rows of rank
+// 16 from 8192 (9.0 : 10.7).
 bool lora_fused(int rows, int K, int rank) {
   if (rank > 32) return false;
   return rows <= 4 && rank <= 16 ? rank * K <= 180224 : rows <= 16 && rank * K <= 65536;

@@ -8,8 +8,10 @@
 // read whole before its barrier, or by its own wave, and written behind it).
 //
 // What bounds it: memory (4099 x 8192 with residual, 269 MB, in 51.5 us, 5.2 TB/s,
-// above a 4 GiB copy's 4.75; 64032 heads of 128, 33 MB, in 7.4 us), for single rows
-// a launch (1 x 4096: 2.6 us).
+// above a 4 GiB copy's 4.75; without, 134 MB in 26.2, 5.1; 64032 heads of 128, 33 MB, in
+// 7.3 us), for single rows a launch (1 x 4096: 2.7 us, 2.4 without residual).  Rows of
+// 520 to 1024 channels leave half or more of their 256 threads without a chunk: 4096 x
+// 1024 takes 5.9 us for 17 MB (2.8 TB/s), 7.8 with the residual (4.3).
 #include "wq_layer.hpp"
 
 namespace wq {

@@ -112,8 +112,8 @@ class DecodeStack:
 
 @dataclasses.dataclass
 class LayerAdapters:
-    """The adapters of one decoder layer's products (None: that product has none).  The gate+up product keeps its
-    activation in its epilogue, which takes no adapter."""
+    """The adapters of one decoder layer's products (None: that product has none).  The gate+up product applies its
+    activation in its epilogue, which takes no adapter: variants that adapt those two projections do not run here."""
     qkv: Optional[LoraBank] = None    # three slices: queries, keys, values (or one)
     o: Optional[LoraBank] = None
     down: Optional[LoraBank] = None
@@ -125,7 +125,8 @@ class CachedStack:
 
     norms: two weights [dim] per layer, before QKV and before gate+up (None: no norms); eps theirs.  rotary: turns
     queries and keys to their rows' positions (None: not at all).  adapters: low-rank adapters per layer, of which each
-    sequence of a step names its own.
+    sequence of a step names its own; their part is added to the product as it was stored (bias and residual with it),
+    so these rows are rounded twice.
 
     A step takes the rows of any number of sequences -- prompts, chunks of them or single tokens -- named as
     everywhere in the cache's functions: block_table, kv_lens (with the step's rows) and cu_q (None: as many rows
